@@ -278,7 +278,9 @@ int retention_abi_version(void);
  * i < nkinds the summed milliseconds ms[i] and the launch count count[i], writes the
  * number of dropped launches to *dropped (if not NULL) and clears the records.
  * Kinds: 0 matrix-core chunkwise pass, 1 its segment-state pre-pass, 2 its segment
- * scan, 3 generic chunkwise kernel, 4 decode step, 5 state copy (empty sequence).
+ * scan, 3 generic chunkwise kernel, 4 decode step, 5 state copy (empty sequence), 6 layer
+ * normalisation, 7 rotary positions, 8 causal convolution, 9 selective scan, 10 its passes
+ * over segments and tiles before that, 11 sums of partial gradients.
  * Errors: RETN_ERR_SHAPE (nkinds < 0), RETN_ERR_NULL, RETN_ERR_HIP.
  */
 retn_status retention_profile_enable(int on);
@@ -318,6 +320,185 @@ retn_status retention_chunkwise_fwd_noalloc(const void* q, const void* k, const 
  */
 retn_status retention_calib_mfma(float* out, int blocks, int waves, int iters, void* stream);
 double retention_calib_mfma_flops(int blocks, int waves, int iters);
+
+/* ------------------------------------------------------------------------------------
+ * Operators that stand around the retention in a block: layer normalisation in front of a
+ * mixer, rotary positions of queries and keys, and a second mixer, the selective scan,
+ * with its short causal convolution.
+ *
+ * They follow the conventions above (device memory, ownership, streams, errors), with:
+ *   Types      activations are RETN_F32 or RETN_BF16 (`dtype`); weights of the normalisation
+ *              and the convolution have the type `wdtype`: RETN_F32, or `dtype`'s.  The
+ *              scan's parameters (A, D, dt_bias) and states are fp32.  Sums, statistics
+ *              and states are held in fp32; each output is rounded once.
+ *   Layout     activations are [B, N, D] (or [rows, D]), channels adjacent.  Where a row
+ *              stride (ld...) is given, it is the distance of two tokens in elements and a
+ *              batch's is N times that, so a column slice of a wider projection is taken
+ *              in place; other tensors are contiguous.  Any element alignment.
+ *   Lengths    `lengths` (optional, [B] int32, device memory): sequence b has its first
+ *              lengths[b] tokens (clamped to 0 .. N); what lies behind them is not read,
+ *              output rows there are left as they were, gradient rows there are zero, and
+ *              a final state is the one behind the last of those tokens.
+ *   Limits     D <= 2^20, B * N < 2^31, B * D < 2^31, B * N * D < 2^34 (rotary: B * N * d
+ *              < 2^32); else RETN_ERR_UNSUPPORTED.
+ * All results are the same from call to call (no atomics).
+ */
+
+/*
+ * Layer normalisation of rows of D elements:
+ *     y = (x - mean) * rstd * weight + bias,   rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   x, y          [rows, D]; y must not overlap an input
+ *   weight, bias  [D], each optional (NULL: ones, zeros)
+ *   mean, rstd    optional outputs [rows] fp32, what layer_norm_bwd takes
+ *   eps           >= 0
+ */
+retn_status layer_norm_fwd(const void* x, const void* weight, const void* bias, void* y,
+                           float* mean, float* rstd, long long rows, int D, float eps,
+                           retn_dtype dtype, retn_dtype wdtype, void* stream);
+
+/*
+ * Backward of layer_norm_fwd for the gradient grad_y of y:
+ *     grad_x = rstd * (v - mean(v) - xh * mean(v * xh)),  v = grad_y * weight,
+ *     xh = (x - mean) * rstd;   grad_weight = sum of grad_y * xh,  grad_bias = sum of grad_y
+ *   mean, rstd              the forward's
+ *   grad_weight, grad_bias  [D] of type wdtype, each optional (NULL: not wanted)
+ *   workspace               layer_norm_bwd_workspace_bytes(...), 16-byte aligned; needed
+ *                           only where grad_weight or grad_bias is given
+ */
+retn_status layer_norm_bwd(const void* x, const void* weight, const float* mean,
+                           const float* rstd, const void* grad_y, void* grad_x,
+                           void* grad_weight, void* grad_bias, long long rows, int D,
+                           retn_dtype dtype, retn_dtype wdtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+size_t layer_norm_bwd_workspace_bytes(long long rows, int D, retn_dtype dtype);
+
+/*
+ * Table of rotations: table[i][j] = magnitude * (cos, sin)((first + i) * freq[j]) for
+ * i < count, j < pairs (fp32 pairs; the angle is formed in fp64).  freq: [pairs] fp64, device
+ * memory.  A caller builds it once for the positions and the frequencies that it uses
+ * (scaled ones for long contexts) and keeps it.
+ */
+retn_status rotary_table(float* table, const double* freq, int pairs, long long first,
+                         long long count, float magnitude, void* stream);
+
+/*
+ * Rotary positions: in each head the pairs of the first `rot` elements turn by their
+ * token's row of the table, (a, b) -> (a c - b s, a s + b c); the other elements pass; all
+ * are scaled by q_scale (k_scale).  interleaved: pair i is (2i, 2i+1), else (i, i + rot/2).
+ *   q, out_q   [B, Hq, N, d],   k, out_k  [B, Hk, N, d] (Hk = 0: no keys, NULL)
+ *   strides    host array of 12: the batch, head and token strides in elements of q, out_q,
+ *              k, out_k (elements of a head are adjacent), so that token-major projections
+ *              are read and written in place.  An output may be exactly its input (same
+ *              pointer and strides); no other overlap, and none inside an output.
+ *   table      [table_len, rot/2, 2] fp32
+ *   positions  optional int64, device memory: [N], or [B, N] if positions_per_batch; NULL:
+ *              token n has position first + n (0 <= first, first + N <= table_len).  A
+ *              position outside 0 .. table_len - 1 turns its row's rotated part into NaN.
+ *   d <= 256, rot even, 2 <= rot <= d
+ */
+retn_status rotary_fwd(const void* q, const void* k, void* out_q, void* out_k,
+                       const long long* strides, const float* table, long long table_len,
+                       const long long* positions, int positions_per_batch, long long first,
+                       int B, int Hq, int Hk, int N, int d, int rot, int interleaved,
+                       float q_scale, float k_scale, retn_dtype dtype, void* stream);
+
+/* Backward of rotary_fwd: the transposed rotation of grad_q and grad_k, same arguments. */
+retn_status rotary_bwd(const void* grad_q, const void* grad_k, void* out_q, void* out_k,
+                       const long long* strides, const float* table, long long table_len,
+                       const long long* positions, int positions_per_batch, long long first,
+                       int B, int Hq, int Hk, int N, int d, int rot, int interleaved,
+                       float q_scale, float k_scale, retn_dtype dtype, void* stream);
+
+/*
+ * Short causal convolution of each channel, K in {2, 3, 4}: with xs = [state_in ; x],
+ *     pre_t = bias + sum_j weight[j] xs_(t+j),  y = silu ? pre * sigmoid(pre) : pre
+ *   x          [B, N, D], token stride ldx;   y  [B, N, D]
+ *   weight     [D, K] (the last column meets the current token);  bias [D], optional
+ *   state_in   optional [B, K-1, D] of x's type: the K-1 tokens before the first, oldest
+ *              first (NULL = zeros);  state_out  optional, same layout: the last K-1 rows of
+ *              xs.  Outputs must not overlap inputs or each other.
+ */
+retn_status causal_conv_fwd(const void* x, long long ldx, const void* weight, const void* bias,
+                            void* y, const void* state_in, void* state_out, const int* lengths,
+                            int B, int N, int D, int K, int silu, retn_dtype dtype,
+                            retn_dtype wdtype, void* stream);
+
+/*
+ * Backward of causal_conv_fwd for grad_y [B, N, D] and, optionally, grad_state_out:
+ * grad_x [B, N, D], and each optional: grad_weight [D, K], grad_bias [D] (of type wdtype),
+ * grad_state_in [B, K-1, D].  workspace: causal_conv_bwd_workspace_bytes(...), 16-byte
+ * aligned; needed only where grad_weight or grad_bias is given.
+ */
+retn_status causal_conv_bwd(const void* x, long long ldx, const void* weight, const void* bias,
+                            const void* state_in, const void* grad_y, const void* grad_state_out,
+                            const int* lengths, void* grad_x, void* grad_weight, void* grad_bias,
+                            void* grad_state_in, int B, int N, int D, int K, int silu,
+                            retn_dtype dtype, retn_dtype wdtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+size_t causal_conv_bwd_workspace_bytes(int B, int N, int D, int K, retn_dtype dtype);
+
+/*
+ * One token: y [B, D] from x [B, D] (row stride ldx) and the state [B, K-1, D], whose rows
+ * move up by one in place.  The state must not overlap anything else.
+ */
+retn_status causal_conv_step(const void* x, long long ldx, const void* weight, const void* bias,
+                             void* state, void* y, int B, int D, int K, int silu,
+                             retn_dtype dtype, retn_dtype wdtype, void* stream);
+
+/*
+ * Selective state-space scan: per channel d (of group d / (D/G)) and state n < S,
+ *     h_t[n] = exp(dt_t A[n]) h_(t-1)[n] + dt_t x_t B_t[n]
+ *     y_t    = (sum_n C_t[n] h_t[n] + Dskip x_t) * (z given: z_t sigmoid(z_t), else 1)
+ * with dt_t = raw_t + dt_bias, or softplus of that.  The diagonal, per-token form of the
+ * gated retention's recurrence: decays per channel and state instead of per head.
+ *   x, dt, z, y    [B, N, D] (z optional), token strides ldx, lddt, ldz; y contiguous
+ *   Bm, Cm         [B, N, G, S], token strides ldb, ldc (the G*S elements adjacent)
+ *   A              [D, S] fp32, finite;  Dskip, dt_bias  [D] fp32, optional
+ *   state_in       optional [B, D, S] fp32 (NULL = zeros);  state_out  optional, may equal
+ *                  state_in, must not overlap anything else
+ *   1 <= S <= 64, G divides D.  workspace: selective_scan_workspace_bytes(...), 16-byte
+ *   aligned (0 where sequences are not cut into segments)
+ */
+retn_status selective_scan_fwd(const void* x, const void* dt, const float* A, const void* Bm,
+                               const void* Cm, const float* Dskip, const void* z,
+                               const float* dt_bias, void* y, const float* state_in,
+                               float* state_out, const int* lengths, long long ldx,
+                               long long lddt, long long ldz, long long ldb, long long ldc,
+                               int B, int N, int D, int G, int S, int softplus,
+                               retn_dtype dtype, void* workspace, size_t workspace_bytes,
+                               void* stream);
+size_t selective_scan_workspace_bytes(int B, int N, int D, int G, int S);
+
+/*
+ * Backward of selective_scan_fwd for grad_y [B, N, D] and, optionally, grad_state_out
+ * [B, D, S] fp32.  Writes grad_x, grad_dt (of raw, before the bias) [B, N, D], grad_z where z
+ * is given, grad_B, grad_C [B, N, G, S] (all contiguous, of type dtype), grad_A [D, S], and
+ * each optional: grad_D, grad_dt_bias [D], grad_state_in [B, D, S] (fp32).  workspace:
+ * selective_scan_bwd_workspace_bytes(...), 16-byte aligned.  Outputs must not overlap
+ * inputs or each other.
+ */
+retn_status selective_scan_bwd(const void* x, const void* dt, const float* A, const void* Bm,
+                               const void* Cm, const float* Dskip, const void* z,
+                               const float* dt_bias, const float* state_in, const void* grad_y,
+                               const float* grad_state_out, const int* lengths, void* grad_x,
+                               void* grad_dt, float* grad_A, void* grad_B, void* grad_C,
+                               float* grad_D, void* grad_z, float* grad_dt_bias,
+                               float* grad_state_in, long long ldx, long long lddt,
+                               long long ldz, long long ldb, long long ldc, int B, int N, int D,
+                               int G, int S, int softplus, retn_dtype dtype, void* workspace,
+                               size_t workspace_bytes, void* stream);
+size_t selective_scan_bwd_workspace_bytes(int B, int N, int D, int G, int S);
+
+/*
+ * One token: x, dt, z, y [B, D], Bm, Cm [B, G, S] (row strides as above), the state [B, D, S]
+ * read and overwritten; it must not overlap anything else.
+ */
+retn_status selective_scan_step(const void* x, const void* dt, const float* A, const void* Bm,
+                                const void* Cm, const float* Dskip, const void* z,
+                                const float* dt_bias, float* state, void* y, long long ldx,
+                                long long lddt, long long ldz, long long ldb, long long ldc,
+                                int B, int D, int G, int S, int softplus, retn_dtype dtype,
+                                void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,10 +1,27 @@
 """MI355X-native retention operator: chunkwise and parallel forward, backward, decode step, gated
-variants, and the gated retention layer around it.
+variants, and the gated retention layer around it; and the operators that stand around a mixer in
+a block: layer normalisation, rotary positions, the short causal convolution and the selective scan.
 
 The operator runs in libretention_fwd.so (hand-written HIP kernels for gfx950) behind
 the C ABI in include/retention.h; this package is its Python binding.  Importing the
 package does not load the library; the first call does, and raises if it is missing.
 """
+from ._block import (  # noqa: F401
+    causal_conv_bwd,
+    causal_conv_fwd,
+    causal_conv_step,
+    layer_norm_bwd,
+    layer_norm_fwd,
+    rotary_bwd,
+    rotary_frequencies,
+    rotary_fwd,
+    rotary_table,
+    scan_bwd_workspace_bytes,
+    scan_workspace_bytes,
+    selective_scan_bwd,
+    selective_scan_fwd,
+    selective_scan_step,
+)
 from ._lib import (  # noqa: F401
     RetentionError,
     bwd_workspace_bytes,
@@ -45,4 +62,18 @@ __all__ = [
     "profile_read",
     "calib_mfma",
     "retention_chunkwise_fwd_noalloc",
+    "causal_conv_bwd",
+    "causal_conv_fwd",
+    "causal_conv_step",
+    "layer_norm_bwd",
+    "layer_norm_fwd",
+    "rotary_bwd",
+    "rotary_frequencies",
+    "rotary_fwd",
+    "rotary_table",
+    "scan_bwd_workspace_bytes",
+    "scan_workspace_bytes",
+    "selective_scan_bwd",
+    "selective_scan_fwd",
+    "selective_scan_step",
 ]

@@ -42,10 +42,26 @@ EXPORTED = (
     "retention_calib_mfma",
     "retention_calib_mfma_flops",
     "retention_chunkwise_fwd_noalloc",
+    "layer_norm_fwd",
+    "layer_norm_bwd",
+    "layer_norm_bwd_workspace_bytes",
+    "rotary_table",
+    "rotary_fwd",
+    "rotary_bwd",
+    "causal_conv_fwd",
+    "causal_conv_bwd",
+    "causal_conv_bwd_workspace_bytes",
+    "causal_conv_step",
+    "selective_scan_fwd",
+    "selective_scan_workspace_bytes",
+    "selective_scan_bwd",
+    "selective_scan_bwd_workspace_bytes",
+    "selective_scan_step",
 )
 
 # Kernel kinds reported by retention_profile_read.
-PROFILE_KINDS = ("chunk_main", "chunk_prepass", "chunk_scan", "chunk_generic", "decode", "state_copy")
+PROFILE_KINDS = ("chunk_main", "chunk_prepass", "chunk_scan", "chunk_generic", "decode", "state_copy", "layer_norm",
+                 "rotary", "causal_conv", "selective_scan", "selective_scan_prepass", "gradient_sums")
 
 
 class RetentionError(RuntimeError):

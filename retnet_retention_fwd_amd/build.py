@@ -20,7 +20,7 @@ LIB_NAME = "libretention_fwd.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["api.cpp", "profile.cpp", "backward.cpp", "generic_chunk.hip", "decode.hip", "mfma_chunk.hip", "chunk64.hip", "chunkw.hip", "calib.hip", "noalloc.hip",
-           "bwd_kernels.hip", "msr.hip"]
+           "bwd_kernels.hip", "msr.hip", "block_api.cpp", "norm.hip", "rotary.hip", "conv.hip", "scan.hip", "scan_bwd.hip"]
 
 # Packed-fp32 instructions are disabled for all device code (the compiler would
 # otherwise form v_pk_* fp32 ops from ordinary float code).

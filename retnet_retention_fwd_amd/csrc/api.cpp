@@ -10,6 +10,7 @@
 #include <stdint.h>
 
 #include "launch.h"
+#include "validate.h"
 
 namespace {
 
@@ -17,24 +18,6 @@ constexpr int kMaxDk = 256;           // dk limit (state slice in LDS / register
 constexpr int kMaxDv = 1024;          // dv limit
 constexpr int kGenericMaxGatedChunk = 1024;  // chunk-local cumsum kept in LDS
 constexpr int kParallelGenericChunk = 64;    // chunk of the generic kernel for the parallel form
-
-struct Range {
-    uintptr_t lo, hi;   // [lo, hi)
-};
-
-Range span(const void* p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + bytes};
-}
-
-bool overlaps(Range a, Range b) {
-    if (a.lo == a.hi || b.lo == b.hi) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
-
-size_t elem_bytes(retn_dtype dt) { return dt == RETN_BF16 ? 2 : 4; }
-
-bool valid_dtype(retn_dtype dt) { return dt == RETN_F32 || dt == RETN_BF16; }
 
 // Shared validation of the chunkwise entry points.
 retn_status validate_chunk(const void* q, const void* k, const void* v, const float* decay,
@@ -69,9 +52,6 @@ retn_status validate_chunk(const void* q, const void* k, const void* v, const fl
 
 // Chunks longer than the sequence are one chunk of N tokens.
 int effective_chunk(int N, int chunk) { return N > 0 ? (chunk < N ? chunk : N) : 1; }
-
-// The matrix-core kernels move 16-byte units of q, k, v and store 8-byte units of o.
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The matrix-core kernels address a head's rows with 32-bit byte offsets; longer
 // heads take the generic kernel, which indexes in 64 bits.
