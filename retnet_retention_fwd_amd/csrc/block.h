@@ -106,9 +106,7 @@ struct ScanArgs {
     float* workspace;
 };
 struct ScanPlan {
-    int cfg;                   // lane layout: channels and states per wave
-    int ch;                    // channels per workgroup
-    int nblk;                  // channel blocks over all groups
+    int nblk;                  // channel blocks (of a wave or a workgroup) over all groups
     int nseg, seg;             // segments per sequence, tokens per segment
     // workspace, in floats
     size_t off_end, off_dt;    // segment end states, then entry states; sums of dt

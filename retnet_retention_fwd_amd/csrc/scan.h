@@ -1,13 +1,10 @@
-// What the scan's forward and backward kernels share: lane layout, staging, reductions.
+// What the scan's forward and backward kernels share.
 //
-// Lanes.  LPC adjacent lanes hold one channel's states, SPL each (4 LPC >= S states): lane
-// = LPC c + q' for channel c of the wave.  A wave of 64 channels-by-state-groups walks over
-// tokens with its states in registers; x, dt and the gates are staged once per (token,
-// channel) in LDS, so their transcendental functions are not repeated in the LPC lanes.
-// With LPC = 4 the state group of a lane is q' with its two bits flipped in odd channels:
-// then lane ^ 7, which one DPP instruction reaches, is the neighbouring channel's lane of
-// the same state group, and sums over channels as well as over a channel's states run on
-// DPP and permlane-swap instructions without LDS.
+// Walks without channel sums (the forward, the backward's first passes) give a lane a
+// channel with all of its S states in registers: nothing is exchanged between lanes, x, dt
+// and the gates are read where they are used, and B and C, the same for all lanes, come
+// through scalar loads as scalar operands (WaveRows).  A wave is 64 channels of one group
+// of one sequence's segment, and needs no other wave: no LDS, no barriers.
 #pragma once
 
 #include "block.h"
@@ -19,116 +16,133 @@ namespace retn {
 namespace {
 
 constexpr int kScanThreads = 256;
+constexpr int kAhead = 8;      // tokens whose loads are issued together, a block ahead
 
-template <int LPC>
-__device__ __forceinline__ int state_group(int lane) {
-    const int q = lane & (LPC - 1);
-    return LPC == 4 ? q ^ ((lane & 4) ? 3 : 0) : q;
-}
-
-// Sums over the LPC lanes of a channel of LPC values each; the lane keeps the sum of value
-// `kept(lane)`.  Mask 7 comes before 1 and 2: its partner then differs in them, later
-// partners agree in what has been kept.
-template <int LPC>
-__device__ __forceinline__ float state_sum(const float* v, int lane) {
-    float t[LPC];
-#pragma unroll
-    for (int i = 0; i < LPC; ++i) t[i] = v[i];
-    if (LPC >= 16) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = pair_sum<8>(t[i], t[(i + 8) & (LPC - 1)], lane & 8);
-    }
-    if (LPC >= 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = pair_sum<7>(t[i], t[(i + 4) & (LPC - 1)], lane & 4);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) t[i] = pair_sum<2>(t[i], t[i + 2], lane & 2);
-    return pair_sum<1>(t[0], t[1], lane & 1);
-}
-// The value that state_sum leaves in a lane is number lane & (LPC - 1).
-
-// One token's dt and its factors for the tile's rows behind `rows`: dt = u = 0 keeps the state.
+// One token's dt.
 __device__ __forceinline__ float step_size(float raw, bool softplus) { return softplus ? softplus_f(raw) : raw; }
 
 __device__ __forceinline__ int scan_length(const int* lengths, int b, int N) {
     if (lengths == nullptr) return N;
-    const int n = lengths[b];
+    const int n = __builtin_amdgcn_readfirstlane(lengths[b]);   // b is the same for all lanes
     return n < 0 ? 0 : n < N ? n : N;
 }
 
-// The workgroup's place: channel block (of one group), segment, sequence.
+// A wave's or workgroup's place: channel block (of one group), segment, sequence.
 struct ScanPlace {
-    int g, c0, cend, seg, b;
+    int g, c0, cend, seg, b, blk;
+    int t_begin, t_full, t_end;   // the segment's tokens, all and those of the sequence
 };
 template <int CH>
-__device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a, int nblk, int nseg, unsigned id) {
-    const int per = nblk / a.G, dg = a.D / a.G, blk = id % nblk;
+__device__ __forceinline__ ScanPlace scan_place(const ScanArgs& a, int nblk, int nseg, int seg, unsigned id) {
+    const int per = nblk / a.G, dg = a.D / a.G;
     const unsigned bs = id / nblk;
     ScanPlace p;
-    p.g = blk / per;
-    p.c0 = p.g * dg + blk % per * CH;
+    p.blk = static_cast<int>(id % nblk);
+    p.g = p.blk / per;
+    p.c0 = p.g * dg + p.blk % per * CH;
     p.cend = (p.g + 1) * dg;
     p.seg = bs % nseg;
     p.b = bs / nseg;
+    const int n = scan_length(a.lengths, p.b, a.N);
+    p.t_begin = p.seg * seg;
+    p.t_full = p.t_begin + seg < a.N ? p.t_begin + seg : a.N;
+    p.t_end = p.t_full < n ? p.t_full : n;
     return p;
 }
+// The place of this wave among all waves of a launch of waves (not of workgroups).
+__device__ __forceinline__ unsigned wave_id() {
+    return __builtin_amdgcn_readfirstlane(blockIdx.x * (kScanThreads / 64) + (threadIdx.x >> 6));
+}
 
-// B and C of a tile's tokens, [TT][SP] in LDS, zeros behind the last state and token.
-template <typename T, int TT, int SP>
-struct StateRows {
-    static constexpr int kPer = (TT * SP + kScanThreads - 1) / kScanThreads;
-    T raw[kPer];
-    __device__ __forceinline__ void load(const T* p, long long ld, int rows, int S) {
+// The S values of B or C of one token, as scalars.  SCALAR: S = SP and every row starts at a
+// multiple of 4 bytes, so they come by scalar loads from constant memory; else a lane loads
+// each and they are read across (S extra vector instructions a token).
+template <typename T, int SP, bool SCALAR>
+struct WaveRow;
+template <int SP>
+struct WaveRow<float, SP, true> {
+    float v[SP];
+    __device__ __forceinline__ void load(const float* p, int) {
+        const auto* c = reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(p));
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int i = threadIdx.x + k * kScanThreads, t = i / SP, n = i % SP;
-            raw[k] = t < rows && n < S ? p[t * ld + n] : T(0);
-        }
+        for (int i = 0; i < SP; ++i) v[i] = c[i];
     }
-    __device__ __forceinline__ void store(float* lds) const {
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+};
+template <int SP>
+struct WaveRow<bf16_t, SP, true> {
+    uint32_t v[SP / 2];
+    __device__ __forceinline__ void load(const bf16_t* p, int) {
+        const auto* c = reinterpret_cast<const __attribute__((address_space(4))) uint32_t*>(reinterpret_cast<uintptr_t>(p));
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int i = threadIdx.x + k * kScanThreads;
-            if (TT * SP % kScanThreads == 0 || i < TT * SP) lds[i] = up(raw[k]);
-        }
+        for (int i = 0; i < SP / 2; ++i) v[i] = c[i];
+    }
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
     }
 };
-
-template <int SPL>
-__device__ __forceinline__ void lds_states(const float* p, float (&out)[SPL]) {
-    if (SPL % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < SPL; i += 4) {
-            const f32v4 v = *reinterpret_cast<const f32v4*>(p + i);
-            out[i] = v.x;
-            out[i + 1] = v.y;
-            out[i + 2] = v.z;
-            out[i + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < SPL; ++i) out[i] = p[i];
+template <typename T, int SP>
+struct WaveRow<T, SP, false> {
+    float v;
+    __device__ __forceinline__ void load(const T* p, int S) {
+        const int lane = threadIdx.x & 63;
+        v = lane < S ? up(p[lane]) : 0.f;
     }
+    __device__ __forceinline__ float get(int i) const {
+        return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
+    }
+};
+// Scalar loads return in any order, so the only wait for one is the wait for all of them.
+// Behind this point the rows loaded so far are there, and the next rows' loads, issued right
+// behind it, have a whole token's work to arrive.
+template <bool SCALAR>
+__device__ __forceinline__ void rows_arrived() {
+    if (!SCALAR) return;
+    __builtin_amdgcn_s_waitcnt(0xC07F);      // lgkmcnt(0), nothing else
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <bool SCALAR>
+__device__ __forceinline__ void rows_issued() {
+    if (SCALAR) __builtin_amdgcn_sched_barrier(0);
 }
 
-// S states of a channel: a lane's SPL of them, from n0, zeros behind the last one.
-template <int SPL>
-__device__ __forceinline__ void load_state(const float* p, int n0, int S, bool on, float (&h)[SPL]) {
-#pragma unroll
-    for (int i = 0; i < SPL; ++i) h[i] = on && n0 + i < S ? p[n0 + i] : 0.f;
+// An element of a row that is the same for all lanes: a scalar address and the lane's byte
+// offset, which one load instruction adds.
+template <typename T>
+__device__ __forceinline__ T row_at(const T* row, uint32_t byte) {
+    return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + byte);
 }
-template <int SPL>
-__device__ __forceinline__ void store_state(float* p, int n0, int S, const float (&h)[SPL]) {
-    if (SPL % 4 == 0 && S % 4 == 0) {
+template <typename T>
+__device__ __forceinline__ void row_put(T* row, uint32_t byte, T v) {
+    *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + byte) = v;
+}
+
+// S states of a channel, zeros behind the last one.
+template <int SP>
+__device__ __forceinline__ void load_state(const float* p, int S, bool on, float (&h)[SP]) {
 #pragma unroll
-        for (int i = 0; i < SPL; i += 4)
-            if (n0 + i < S) *reinterpret_cast<Raw<float, 4>*>(p + n0 + i) = Raw<float, 4>{{h[i], h[i + 1], h[i + 2], h[i + 3]}};
-        return;
+    for (int i = 0; i < SP; i += 4) {
+        Raw<float, 4> r = {};
+        if (on && i < S) r = raw_load_n<float, 4>(p + i, S - i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i + j] = r.v[j];
     }
+}
+template <int SP>
+__device__ __forceinline__ void store_state(float* p, int S, const float (&h)[SP]) {
 #pragma unroll
-    for (int i = 0; i < SPL; ++i)
-        if (n0 + i < S) p[n0 + i] = h[i];
+    for (int i = 0; i < SP; i += 4)
+        if (i < S) raw_store_n<float, 4>(p + i, Raw<float, 4>{{h[i], h[i + 1], h[i + 2], h[i + 3]}}, S - i);
+}
+
+// Whether B's and C's rows can be read by scalar loads (WaveRow).
+inline bool scalar_rows(const ScanArgs& a, int SP) {
+    if (a.S != SP) return false;
+    const size_t es = a.bf16 ? 2 : 4;
+    auto even = [&](const void* p, long long ld) {
+        return (reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * es)) % 4 == 0;
+    };
+    return even(a.Bm, a.ldb) && even(a.Cm, a.ldc);
 }
 
 }  // namespace

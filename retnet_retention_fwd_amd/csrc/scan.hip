@@ -3,16 +3,13 @@
 //     y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t),      dt = softplus(raw + bias)
 //
 // Bound by the vector ALUs: an exponential and four multiply-adds per (token, channel,
-// state), where HBM moves eight bytes per (token, channel).  The states stay in registers
-// (scan.h has the lane layout), tokens come in tiles of 32 that are staged in LDS: dt and
-// dt x once per (token, channel), B and C once per token.  The next tile's global loads are
-// in flight while a tile is walked; y goes back through LDS so that its gating and its
-// store run on packs of channels.
+// state), where HBM moves eight bytes per (token, channel).  A lane walks over the tokens of
+// one channel with all of its states in registers (scan.h).
 //
-// Few channels leave most of the chip idle, so a sequence is then cut into segments: a
-// first pass walks every segment but the last from a zero state, keeping its end state
-// and the sum of its dt (the segment's whole decay is exp(A sum dt)), a small kernel
-// composes the entry states, and the main pass walks all segments at once.
+// Few channels leave most of the chip idle, so a sequence is cut into segments: a first
+// pass walks every segment but the last from a zero state, keeping its end state and the
+// sum of its dt (the segment's whole decay is exp(A sum dt)), a small kernel composes the
+// entry states, and the main pass walks all segments at once.
 
 #include "scan.h"
 
@@ -20,138 +17,135 @@ namespace retn {
 
 namespace {
 
-constexpr int kTile = 32;      // tokens of a tile
-
 // STATE: the first pass of a segmented sequence, no y.
-template <typename T, int LPC, int SPL, bool STATE>
+template <typename T, int SP, bool SCALAR, bool STATE>
 __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, ScanPlan pl) {
-    constexpr int CH = kScanThreads / LPC, SP = LPC * SPL, CQ = CH / 4;   // channels, states, packs of 4 channels
-    constexpr int UNITS = kTile * CQ, NU = (UNITS + kScanThreads - 1) / kScanThreads;
-    static_assert(UNITS % kScanThreads == 0 || NU == 1, "units fill the workgroup or run in one pass");
-    __shared__ float sdt[kTile][CH], su[kTile][CH], sy[STATE ? 1 : kTile][CH];
-    __shared__ __attribute__((aligned(16))) float sB[kTile * SP], sC[STATE ? 4 : kTile * SP];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const ScanPlace p = scan_place<CH>(a, pl.nblk, STATE ? pl.nseg - 1 : pl.nseg, blockIdx.x);
-    const int n = scan_length(a.lengths, p.b, a.N);
-    const int t_begin = p.seg * pl.seg, t_full = t_begin + pl.seg < a.N ? t_begin + pl.seg : a.N;
-    const int t_end = t_full < n ? t_full : n;
-    // this lane's channel and states
-    const int cl = tid / LPC, ch = p.c0 + cl, n0 = state_group<LPC>(lane) * SPL;
-    const bool on = ch < p.cend;
-    float A2[SPL], h[SPL];
+    const unsigned id = wave_id();
+    const int nseg = STATE ? pl.nseg - 1 : pl.nseg;
+    if (id >= static_cast<unsigned>(pl.nblk) * nseg * a.B) return;
+    const ScanPlace p = scan_place<64>(a, pl.nblk, nseg, pl.seg, id);
+    const int c = p.c0 + (threadIdx.x & 63), S = SCALAR ? SP : a.S;
+    const bool on = c < p.cend;
+    const int ch = on ? c : p.cend - 1;        // idle lanes repeat the last channel and store nothing
+    float A2[SP], h[SP];
+    load_state<SP>(a.A + static_cast<size_t>(ch) * S, S, true, A2);
 #pragma unroll
-    for (int i = 0; i < SPL; ++i)
-        A2[i] = on && n0 + i < a.S ? a.A[static_cast<size_t>(ch) * a.S + n0 + i] * kLog2e : 0.f;
+    for (int i = 0; i < SP; ++i) A2[i] *= kLog2e;
     const size_t bd = static_cast<size_t>(p.b) * a.D + ch;
     const size_t slot = (static_cast<size_t>(p.b) * pl.nseg + p.seg) * a.D + ch;   // (sequence, segment, channel)
-    if (STATE || (pl.nseg == 1 && a.state_in == nullptr)) {
-#pragma unroll
-        for (int i = 0; i < SPL; ++i) h[i] = 0.f;
-    } else if (pl.nseg == 1) {
-        load_state<SPL>(a.state_in + bd * a.S, n0, a.S, on, h);
-    } else {
-        load_state<SPL>(a.workspace + pl.off_end + slot * a.S, n0, a.S, on, h);
-    }
+    const float* from = STATE ? nullptr : pl.nseg > 1 ? a.workspace + pl.off_end + slot * S
+                        : a.state_in != nullptr       ? a.state_in + bd * S
+                                                      : nullptr;
+    load_state<SP>(from, S, from != nullptr, h);
+    const float bias = a.bias != nullptr ? a.bias[ch] : 0.f, skip = a.Dskip != nullptr ? a.Dskip[ch] : 0.f;
     float dsum = 0.f;
-
-    // this thread's packs of 4 channels: all of its tokens in the same channels
-    const int cq = tid % CQ, uc = p.c0 + 4 * cq, left = p.cend - uc;
-    float bias[4], skip[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        bias[i] = a.bias != nullptr && i < left ? a.bias[uc + i] : 0.f;
-        skip[i] = a.Dskip != nullptr && i < left ? a.Dskip[uc + i] : 0.f;
-    }
-    Raw<T, 4> rx[NU], rdt[NU], rz[NU], cx[NU], cz[NU];
-    StateRows<T, kTile, SP> rB, rC;
     const size_t tok0 = static_cast<size_t>(p.b) * a.N;
-    auto fetch = [&](int t0) {
-        const int rows = t_end - t0;
+    // rows of the sequence, the same for all lanes; a lane adds its channel
+    const T* xp = static_cast<const T*>(a.x) + tok0 * a.ldx;
+    const T* dp = static_cast<const T*>(a.dt) + tok0 * a.lddt;
+    const T* zp = static_cast<const T*>(a.z) + tok0 * a.ldz;
+    const T* Bp = static_cast<const T*>(a.Bm) + tok0 * a.ldb + p.g * S;
+    const T* Cp = static_cast<const T*>(a.Cm) + tok0 * a.ldc + p.g * S;
+    T* yp = static_cast<T*>(a.y) + tok0 * a.D;
+    const uint32_t at = static_cast<uint32_t>(ch) * sizeof(T);
+    const bool gated = !STATE && a.z != nullptr;
+
+    // one token's step of all states; its read-out
+    auto step = [&](float dt, float x, const WaveRow<T, SP, SCALAR>& B, const WaveRow<T, SP, SCALAR>& C) {
+        const float u = dt * x;
+        float y0 = skip * x, y1 = 0.f;
 #pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int r = (tid + k * kScanThreads) / CQ;
-            rx[k] = rdt[k] = rz[k] = Raw<T, 4>{};
-            if (r < rows && r < kTile && left > 0) {
-                const size_t t = tok0 + t0 + r;
-                rx[k] = raw_load_n<T, 4>(static_cast<const T*>(a.x) + t * a.ldx + uc, left);
-                rdt[k] = raw_load_n<T, 4>(static_cast<const T*>(a.dt) + t * a.lddt + uc, left);
-                if (!STATE && a.z != nullptr) rz[k] = raw_load_n<T, 4>(static_cast<const T*>(a.z) + t * a.ldz + uc, left);
-            }
+        for (int i = 0; i < SP; ++i) {
+            h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], u * B.get(i));
+            if (!STATE) (i & 1 ? y1 : y0) = fmaf(C.get(i), h[i], i & 1 ? y1 : y0);
         }
-        rB.load(static_cast<const T*>(a.Bm) + (tok0 + t0) * a.ldb + p.g * a.S, a.ldb, rows, a.S);
-        if (!STATE) rC.load(static_cast<const T*>(a.Cm) + (tok0 + t0) * a.ldc + p.g * a.S, a.ldc, rows, a.S);
+        dsum += dt;
+        return y0 + y1;
     };
-    if (t_begin < t_end) fetch(t_begin);
-    for (int t0 = t_begin; t0 < t_end; t0 += kTile) {
-        const int rows = t_end - t0 < kTile ? t_end - t0 : kTile;
+    auto gate = [&](float z) { return z * sigmoid_f(z); };
+
+    T rx[kAhead], rdt[kAhead], rz[kAhead] = {};
+    auto fetch = [&](int t0) {
+        const T* xr = xp + t0 * a.ldx;
+        const T* dr = dp + t0 * a.lddt;
+        const T* zr = zp + t0 * a.ldz;
 #pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int r = (tid + k * kScanThreads) / CQ;
-            if (UNITS % kScanThreads == 0 || r < kTile) {
-                f32v4 d, u;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float v = r < rows ? step_size(up(rdt[k].v[i]) + bias[i], a.softplus) : 0.f;
-                    d[i] = v;
-                    u[i] = v * up(rx[k].v[i]);
-                }
-                *reinterpret_cast<f32v4*>(&sdt[r][4 * cq]) = d;
-                *reinterpret_cast<f32v4*>(&su[r][4 * cq]) = u;
-            }
-            cx[k] = rx[k];
-            cz[k] = rz[k];
+        for (int k = 0; k < kAhead; ++k) {
+            rx[k] = row_at(xr, at);
+            rdt[k] = row_at(dr, at);
+            xr += a.ldx;
+            dr += a.lddt;
         }
-        rB.store(sB);
-        if (!STATE) rC.store(sC);
-        __syncthreads();
-        if (t0 + kTile < t_end) fetch(t0 + kTile);
+        if (gated) {
 #pragma unroll
-        for (int tb = 0; tb < kTile; tb += LPC) {
-            float part[LPC];
-#pragma unroll
-            for (int j = 0; j < LPC; ++j) {
-                const int t = tb + j;
-                const float dt = sdt[t][cl], u = su[t][cl];
-                float Bv[SPL], Cv[SPL];
-                lds_states<SPL>(sB + t * SP + n0, Bv);
-                if (!STATE) lds_states<SPL>(sC + t * SP + n0, Cv);
-                if (STATE) dsum += dt;
-                float y = 0.f;
-#pragma unroll
-                for (int i = 0; i < SPL; ++i) {
-                    h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], u * Bv[i]);
-                    if (!STATE) y = fmaf(Cv[i], h[i], y);
-                }
-                part[j] = y;
-            }
-            if (!STATE) sy[tb + (lane & (LPC - 1))][cl] = state_sum<LPC>(part, lane);
-        }
-        __syncthreads();
-        if (!STATE) {
-#pragma unroll
-            for (int k = 0; k < NU; ++k) {
-                const int r = (tid + k * kScanThreads) / CQ;
-                if (r >= rows || left <= 0) continue;
-                const f32v4 s = *reinterpret_cast<const f32v4*>(&sy[r][4 * cq]);
-                float o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o[i] = fmaf(skip[i], up(cx[k].v[i]), s[i]);
-                    if (a.z != nullptr) {
-                        const float z = up(cz[k].v[i]);
-                        o[i] *= z * sigmoid_f(z);
-                    }
-                }
-                store_n<T, 4>(static_cast<T*>(a.y) + (tok0 + t0 + r) * a.D + uc, o, left);
+            for (int k = 0; k < kAhead; ++k) {
+                rz[k] = row_at(zr, at);
+                zr += a.ldz;
             }
         }
+    };
+    int t = p.t_begin;
+    if (t + kAhead <= p.t_end) fetch(t);
+    for (; t + kAhead <= p.t_end; t += kAhead) {
+        // the block's steps and, behind them, its gates are taken together, so that the tokens
+        // between them are straight code
+        float x[kAhead], dt[kAhead], z[kAhead], y[kAhead];
+        WaveRow<T, SP, SCALAR> B[2], C[2];
+        const T* Bt = Bp + static_cast<size_t>(t) * a.ldb;
+        const T* Ct = Cp + static_cast<size_t>(t) * a.ldc;
+        B[0].load(Bt, S);
+        if (!STATE) C[0].load(Ct, S);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            x[k] = up(rx[k]);
+            dt[k] = up(rdt[k]) + bias;
+            z[k] = up(rz[k]);
+        }
+        if (t + 2 * kAhead <= p.t_end) fetch(t + kAhead);
+        if (a.softplus) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) dt[k] = softplus_f(dt[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            rows_arrived<SCALAR>();
+            if (k + 1 < kAhead) {
+                B[(k + 1) & 1].load(Bt += a.ldb, S);
+                if (!STATE) C[(k + 1) & 1].load(Ct += a.ldc, S);
+            }
+            rows_issued<SCALAR>();
+            y[k] = step(dt[k], x[k], B[k & 1], C[k & 1]);
+        }
+        if (STATE) continue;
+        if (gated) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) y[k] *= gate(z[k]);
+        }
+        if (on) {
+            T* yr = yp + static_cast<size_t>(t) * a.D;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                row_put(yr, at, down<T>(y[k]));
+                yr += a.D;
+            }
+        }
+    }
+    for (; t < p.t_end; ++t) {
+        WaveRow<T, SP, SCALAR> B, C;
+        B.load(Bp + static_cast<size_t>(t) * a.ldb, S);
+        if (!STATE) C.load(Cp + static_cast<size_t>(t) * a.ldc, S);
+        const size_t tt = t;
+        float y = step(step_size(up(row_at(dp + tt * a.lddt, at)) + bias, a.softplus), up(row_at(xp + tt * a.ldx, at)), B, C);
+        if (STATE) continue;
+        if (gated) y *= gate(up(row_at(zp + tt * a.ldz, at)));
+        if (on) row_put(yp + tt * a.D, at, down<T>(y));
     }
     if (!on) return;
     if (STATE) {
-        store_state<SPL>(a.workspace + pl.off_end + slot * a.S, n0, a.S, h);
-        if (n0 == 0) a.workspace[pl.off_dt + slot] = dsum;
+        store_state<SP>(a.workspace + pl.off_end + slot * S, S, h);
+        a.workspace[pl.off_dt + slot] = dsum;
     } else if (p.seg == pl.nseg - 1 && a.state_out != nullptr) {
-        store_state<SPL>(a.state_out + bd * a.S, n0, a.S, h);
+        store_state<SP>(a.state_out + bd * S, S, h);
     }
 }
 
@@ -164,10 +158,21 @@ __global__ __launch_bounds__(kScanThreads) void scan_compose_kernel(ScanArgs a, 
     float* end = a.workspace + pl.off_end + b * pl.nseg * ds + e;
     const float* sum = a.workspace + pl.off_dt + b * pl.nseg * a.D + e / a.S;
     float h = a.state_in != nullptr ? a.state_in[id] : 0.f;
-    for (int s = 0; s < pl.nseg - 1; ++s) {
-        const float own = end[s * ds];
-        end[s * ds] = h;
-        h = fmaf(exp2_fast(A2 * sum[static_cast<size_t>(s) * a.D]), h, own);
+    constexpr int U = 4;           // segments whose loads are in flight together
+    for (int s0 = 0; s0 < pl.nseg - 1; s0 += U) {
+        float own[U], dt[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const bool in = s0 + k < pl.nseg - 1;
+            own[k] = in ? end[(s0 + k) * ds] : 0.f;
+            dt[k] = in ? sum[static_cast<size_t>(s0 + k) * a.D] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (s0 + k >= pl.nseg - 1) break;
+            end[(s0 + k) * ds] = h;
+            h = fmaf(exp2_fast(A2 * dt[k]), h, own[k]);
+        }
     }
     end[(pl.nseg - 1) * ds] = h;
 }
@@ -214,29 +219,34 @@ __global__ __launch_bounds__(kScanThreads) void scan_step_kernel(ScanArgs a) {
     static_cast<T*>(a.y)[bd] = down<T>(y);
 }
 
-template <typename T, int LPC, int SPL>
+template <typename T, int SP, bool SCALAR>
 hipError_t fwd_cfg(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
     const dim3 block(kScanThreads);
+    constexpr unsigned wpg = kScanThreads / 64;
+    const unsigned waves = static_cast<unsigned>(p.nblk) * a.B;
     if (p.nseg > 1) {
-        {
-            ProfScope prof(kProfScanPre, st);
-            hipLaunchKernelGGL((scan_fwd_kernel<T, LPC, SPL, true>),
-                               dim3(static_cast<unsigned>(p.nblk) * (p.nseg - 1) * a.B), block, 0, st, a, p);
-        }
-        const size_t n = static_cast<size_t>(a.B) * a.D * a.S;
         ProfScope prof(kProfScanPre, st);
+        hipLaunchKernelGGL((scan_fwd_kernel<T, SP, SCALAR, true>), dim3((waves * (p.nseg - 1) + wpg - 1) / wpg), block, 0, st,
+                           a, p);
+        const size_t n = static_cast<size_t>(a.B) * a.D * a.S;
         hipLaunchKernelGGL(scan_compose_kernel, dim3(static_cast<unsigned>((n + kScanThreads - 1) / kScanThreads)), block, 0,
                            st, a, p);
     }
     ProfScope prof(kProfSelScan, st);
-    hipLaunchKernelGGL((scan_fwd_kernel<T, LPC, SPL, false>), dim3(static_cast<unsigned>(p.nblk) * p.nseg * a.B), block, 0,
-                       st, a, p);
+    hipLaunchKernelGGL((scan_fwd_kernel<T, SP, SCALAR, false>), dim3((waves * p.nseg + wpg - 1) / wpg), block, 0, st, a, p);
     return hipGetLastError();
+}
+
+template <typename T, int SP>
+hipError_t fwd_states(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
+    return scalar_rows(a, SP) ? fwd_cfg<T, SP, true>(a, p, st) : fwd_cfg<T, SP, false>(a, p, st);
 }
 
 template <typename T>
 hipError_t fwd_typed(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
-    return p.cfg == 0 ? fwd_cfg<T, 4, 4>(a, p, st) : p.cfg == 1 ? fwd_cfg<T, 8, 4>(a, p, st) : fwd_cfg<T, 16, 4>(a, p, st);
+    if (a.S <= 8) return fwd_states<T, 8>(a, p, st);
+    if (a.S <= 16) return fwd_states<T, 16>(a, p, st);
+    return a.S <= 32 ? fwd_states<T, 32>(a, p, st) : fwd_states<T, 64>(a, p, st);
 }
 
 template <typename T>
@@ -259,17 +269,14 @@ hipError_t step_typed(const ScanArgs& a, hipStream_t st) {
 
 ScanPlan scan_fwd_plan(int B, int N, int D, int G, int S) {
     ScanPlan p{};
-    p.cfg = S <= 16 ? 0 : S <= 32 ? 1 : 2;
-    p.ch = p.cfg == 0 ? 64 : p.cfg == 1 ? 32 : 16;
-    p.nblk = G * ((D / G + p.ch - 1) / p.ch);
-    // Segments: as many as bring the chip four workgroups a CU, of four tiles at least.
-    const size_t wgs = static_cast<size_t>(p.nblk) * (B > 0 ? B : 1);
-    const int most = N / (4 * kTile) > 1 ? N / (4 * kTile) : 1;
-    int want = wgs >= 512 ? 1 : static_cast<int>((1024 + wgs - 1) / wgs);
+    p.nblk = G * ((D / G + 63) / 64);
+    // Segments: as many as bring the chip four waves a SIMD, of 64 tokens at least.
+    const size_t waves = static_cast<size_t>(p.nblk) * (B > 0 ? B : 1);
+    int want = waves >= 2048 ? 1 : static_cast<int>((4096 + waves - 1) / waves);
+    const int most = N / 64 > 1 ? N / 64 : 1;
     if (want > most) want = most;
-    const int tiles = (N + kTile - 1) / kTile;
-    const int per = want > 0 ? (tiles + want - 1) / want : tiles;
-    p.seg = per > 0 ? per * kTile : kTile;
+    const int steps = (N + kAhead - 1) / kAhead, per = (steps + want - 1) / want;
+    p.seg = per > 0 ? per * kAhead : kAhead;
     p.nseg = N > 0 ? (N - 1) / p.seg + 1 : 1;
     const size_t bs = static_cast<size_t>(B) * p.nseg * D;
     p.off_end = 0;

@@ -6,14 +6,18 @@
 //     dA = sum_t q dt,        dB_t = sum_channels w dt x,   dC_t = sum_channels g h_t,
 //     dD = sum g x,           dz = gy (C.h + D x) silu'(z).
 //
-// Bound by the vector ALUs, like the forward.  A first pass walks forward and keeps the
-// state in front of every 16th token; the main pass takes tiles of 16 tokens from the last
-// to the first, recomputes the tile's states and decays into registers and walks back
-// through them.  So no state but one in 16 is ever in memory and an exponential is taken
-// twice per (token, channel, state) in all.  dB and dC sum over channels: over a wave's in
-// registers (two instructions a value, scan.h), over a workgroup's in LDS, over workgroups
-// by a second kernel in a fixed order; the parameters' sums over tokens stay in registers
-// until the end of a segment.
+// Bound by the vector ALUs, like the forward.  A first pass walks forward (a lane a channel,
+// scan.h) and keeps the state in front of every 16th token; the main pass takes tiles of 16
+// tokens from the last to the first.  It recomputes the states and decays of half a tile into
+// registers and walks back through them, so no state but one in 16 is ever in memory and an
+// exponential is taken two and a half times per (token, channel, state) in all.
+//
+// dB and dC sum over channels, so the main pass spreads a channel's states over LPC lanes, four
+// each: few enough to keep eight tokens of them, and lanes of the same states are then the
+// ones to sum over.  A wave sums its channels' terms in registers (permlane swaps and DPP), a
+// workgroup its waves' in LDS, a second kernel the workgroups' in a fixed order.  Everything
+// that is per (token, channel) is computed once for the tile and kept in LDS.  The parameters'
+// sums over tokens stay in registers until the end of a segment.
 //
 // Segments, where channels are few: the first pass walks each from a zero state, a second
 // one walks the adjoint back through each from zero, and a small kernel composes both into
@@ -26,181 +30,197 @@ namespace retn {
 namespace {
 
 constexpr int kTile = 16;      // tokens of a tile, and between kept states
-constexpr int SPL = 4;
+constexpr int kPart = 4;       // tokens whose states and decays are in registers together
+constexpr size_t kWantWaves = 2048;
+constexpr int SPL = 4;         // states of a lane in the main pass
 
 // The state in front of each tile, its segment walked from zero, and the sum of dt from the
 // segment's first token to there; the end state and whole sum of dt go to the segment's slot.
-template <typename T, int LPC>
+template <typename T, int SP, bool SCALAR>
 __global__ __launch_bounds__(kScanThreads) void scan_keep_kernel(ScanArgs a, ScanPlan pl) {
-    constexpr int CH = kScanThreads / LPC, SP = LPC * SPL, CQ = CH / 4, TT = 2 * kTile;
-    constexpr int UNITS = TT * CQ, NU = (UNITS + kScanThreads - 1) / kScanThreads;
-    __shared__ float sdt[TT][CH], su[TT][CH];
-    __shared__ __attribute__((aligned(16))) float sB[TT * SP];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const ScanPlace p = scan_place<CH>(a, pl.nblk, pl.nseg, blockIdx.x);
-    const int n = scan_length(a.lengths, p.b, a.N);
-    const int t_begin = p.seg * pl.seg, t_full = t_begin + pl.seg < a.N ? t_begin + pl.seg : a.N;
-    const int t_end = t_full < n ? t_full : n;
-    const int cl = tid / LPC, ch = p.c0 + cl, n0 = state_group<LPC>(lane) * SPL;
-    const bool on = ch < p.cend;
-    float A2[SPL], h[SPL], dsum = 0.f;
+    const unsigned id = wave_id();
+    const int nblk = a.G * ((a.D / a.G + 63) / 64);
+    if (id >= static_cast<unsigned>(nblk) * pl.nseg * a.B) return;
+    const ScanPlace p = scan_place<64>(a, nblk, pl.nseg, pl.seg, id);
+    const int c = p.c0 + (threadIdx.x & 63), S = SCALAR ? SP : a.S;
+    const bool on = c < p.cend;
+    const int ch = on ? c : p.cend - 1;
+    float A2[SP], h[SP], dsum = 0.f;
+    load_state<SP>(a.A + static_cast<size_t>(ch) * S, S, true, A2);
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-        A2[i] = on && n0 + i < a.S ? a.A[static_cast<size_t>(ch) * a.S + n0 + i] * kLog2e : 0.f;
+    for (int i = 0; i < SP; ++i) {
+        A2[i] *= kLog2e;
         h[i] = 0.f;
     }
-    const size_t slot = (static_cast<size_t>(p.b) * pl.nseg + p.seg) * a.D + ch;
     const int tiles = (a.N + kTile - 1) / kTile;
-    const int cq = tid % CQ, uc = p.c0 + 4 * cq, left = p.cend - uc;
-    float bias[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bias[i] = a.bias != nullptr && i < left ? a.bias[uc + i] : 0.f;
-    Raw<T, 4> rx[NU], rdt[NU];
-    StateRows<T, TT, SP> rB;
+    const float bias = a.bias != nullptr ? a.bias[ch] : 0.f;
     const size_t tok0 = static_cast<size_t>(p.b) * a.N;
-    auto fetch = [&](int t0) {
-        const int rows = t_end - t0;
+    const T* xp = static_cast<const T*>(a.x) + tok0 * a.ldx;
+    const T* dp = static_cast<const T*>(a.dt) + tok0 * a.lddt;
+    const uint32_t lane_at = static_cast<uint32_t>(ch) * sizeof(T);
+    const T* Bp = static_cast<const T*>(a.Bm) + tok0 * a.ldb + p.g * S;
+    auto step = [&](float dt, float x, const WaveRow<T, SP, SCALAR>& B) {
+        const float u = dt * x;
 #pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int r = (tid + k * kScanThreads) / CQ;
-            rx[k] = rdt[k] = Raw<T, 4>{};
-            if (r < rows && r < TT && left > 0) {
-                const size_t t = tok0 + t0 + r;
-                rx[k] = raw_load_n<T, 4>(static_cast<const T*>(a.x) + t * a.ldx + uc, left);
-                rdt[k] = raw_load_n<T, 4>(static_cast<const T*>(a.dt) + t * a.lddt + uc, left);
-            }
-        }
-        rB.load(static_cast<const T*>(a.Bm) + (tok0 + t0) * a.ldb + p.g * a.S, a.ldb, rows, a.S);
+        for (int i = 0; i < SP; ++i) h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], u * B.get(i));
+        dsum += dt;
     };
     auto keep = [&](int t) {
         if (!on) return;
         const size_t at = (static_cast<size_t>(p.b) * tiles + t / kTile) * a.D + ch;
-        store_state<SPL>(a.workspace + pl.off_ckpt + at * a.S, n0, a.S, h);
-        if (n0 == 0) a.workspace[pl.off_cum + at] = dsum;
+        store_state<SP>(a.workspace + pl.off_ckpt + at * S, S, h);
+        a.workspace[pl.off_cum + at] = dsum;
     };
-    if (t_begin < t_end) fetch(t_begin);
-    for (int t0 = t_begin; t0 < t_end; t0 += TT) {
-        const int rows = t_end - t0 < TT ? t_end - t0 : TT;
+    T rx[kAhead], rdt[kAhead];
+    auto fetch = [&](int t0) {
+        const T* xr = xp + t0 * a.ldx;
+        const T* dr = dp + t0 * a.lddt;
 #pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int r = (tid + k * kScanThreads) / CQ;
-            if (UNITS % kScanThreads == 0 || r < TT) {
-                f32v4 d, u;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    d[i] = r < rows ? step_size(up(rdt[k].v[i]) + bias[i], a.softplus) : 0.f;
-                    u[i] = d[i] * up(rx[k].v[i]);
-                }
-                *reinterpret_cast<f32v4*>(&sdt[r][4 * cq]) = d;
-                *reinterpret_cast<f32v4*>(&su[r][4 * cq]) = u;
-            }
+        for (int k = 0; k < kAhead; ++k) {
+            rx[k] = row_at(xr, lane_at);
+            rdt[k] = row_at(dr, lane_at);
+            xr += a.ldx;
+            dr += a.lddt;
         }
-        rB.store(sB);
-        __syncthreads();
-        if (t0 + TT < t_end) fetch(t0 + TT);
+    };
+    int t = p.t_begin;
+    if (t + kAhead <= p.t_end) fetch(t);
+    for (; t + kAhead <= p.t_end; t += kAhead) {
+        if (t % kTile == 0) keep(t);
+        float x[kAhead], dt[kAhead];
+        WaveRow<T, SP, SCALAR> B[2];
+        const T* Bt = Bp + static_cast<size_t>(t) * a.ldb;
+        B[0].load(Bt, S);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (t0 + half * kTile >= t_end) break;
-            keep(t0 + half * kTile);
-#pragma unroll
-            for (int j = 0; j < kTile; ++j) {
-                const int t = half * kTile + j;
-                const float dt = sdt[t][cl], u = su[t][cl];
-                float Bv[SPL];
-                lds_states<SPL>(sB + t * SP + n0, Bv);
-                dsum += dt;
-#pragma unroll
-                for (int i = 0; i < SPL; ++i) h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], u * Bv[i]);
-            }
+        for (int k = 0; k < kAhead; ++k) {
+            x[k] = up(rx[k]);
+            dt[k] = up(rdt[k]) + bias;
         }
-        __syncthreads();
+        if (t + 2 * kAhead <= p.t_end) fetch(t + kAhead);
+        if (a.softplus) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) dt[k] = softplus_f(dt[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            rows_arrived<SCALAR>();
+            if (k + 1 < kAhead) B[(k + 1) & 1].load(Bt += a.ldb, S);
+            rows_issued<SCALAR>();
+            step(dt[k], x[k], B[k & 1]);
+        }
+    }
+    for (; t < p.t_end; ++t) {
+        if (t % kTile == 0) keep(t);
+        WaveRow<T, SP, SCALAR> B;
+        B.load(Bp + static_cast<size_t>(t) * a.ldb, S);
+        const size_t tt = t;
+        step(step_size(up(row_at(dp + tt * a.lddt, lane_at)) + bias, a.softplus), up(row_at(xp + tt * a.ldx, lane_at)), B);
     }
     if (!on || pl.nseg == 1) return;
-    store_state<SPL>(a.workspace + pl.off_end + slot * a.S, n0, a.S, h);
-    if (n0 == 0) a.workspace[pl.off_dt + slot] = dsum;
+    const size_t slot = (static_cast<size_t>(p.b) * pl.nseg + p.seg) * a.D + ch;
+    store_state<SP>(a.workspace + pl.off_end + slot * S, S, h);
+    a.workspace[pl.off_dt + slot] = dsum;
 }
 
 // The adjoint that leaves each segment but the first at its front, from zero behind its end.
-template <typename T, int LPC>
+template <typename T, int SP, bool SCALAR>
 __global__ __launch_bounds__(kScanThreads) void scan_rev_kernel(ScanArgs a, ScanPlan pl) {
-    constexpr int CH = kScanThreads / LPC, SP = LPC * SPL, CQ = CH / 4, TT = 2 * kTile;
-    constexpr int UNITS = TT * CQ, NU = (UNITS + kScanThreads - 1) / kScanThreads;
-    __shared__ float sdt[TT][CH], sg[TT][CH];
-    __shared__ __attribute__((aligned(16))) float sC[TT * SP];
-    const int tid = threadIdx.x, lane = tid & 63;
-    ScanPlace p = scan_place<CH>(a, pl.nblk, pl.nseg - 1, blockIdx.x);
-    p.seg += 1;
+    const unsigned id = wave_id();
+    const int nblk = a.G * ((a.D / a.G + 63) / 64);
+    if (id >= static_cast<unsigned>(nblk) * (pl.nseg - 1) * a.B) return;
+    ScanPlace p = scan_place<64>(a, nblk, pl.nseg - 1, pl.seg, id);
+    p.seg += 1;                                // the place of the segment behind
+    p.t_begin = p.seg * pl.seg;
+    p.t_full = p.t_begin + pl.seg < a.N ? p.t_begin + pl.seg : a.N;
     const int n = scan_length(a.lengths, p.b, a.N);
-    const int t_begin = p.seg * pl.seg, t_full = t_begin + pl.seg < a.N ? t_begin + pl.seg : a.N;
-    const int t_end = t_full < n ? t_full : n;
-    const int cl = tid / LPC, ch = p.c0 + cl, n0 = state_group<LPC>(lane) * SPL;
-    const bool on = ch < p.cend;
-    float A2[SPL], w[SPL];
+    p.t_end = p.t_full < n ? p.t_full : n;
+    const int c = p.c0 + (threadIdx.x & 63), S = SCALAR ? SP : a.S;
+    const bool on = c < p.cend;
+    const int ch = on ? c : p.cend - 1;
+    float A2[SP], w[SP];
+    load_state<SP>(a.A + static_cast<size_t>(ch) * S, S, true, A2);
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-        A2[i] = on && n0 + i < a.S ? a.A[static_cast<size_t>(ch) * a.S + n0 + i] * kLog2e : 0.f;
+    for (int i = 0; i < SP; ++i) {
+        A2[i] *= kLog2e;
         w[i] = 0.f;
     }
-    const int cq = tid % CQ, uc = p.c0 + 4 * cq, left = p.cend - uc;
-    float bias[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bias[i] = a.bias != nullptr && i < left ? a.bias[uc + i] : 0.f;
-    Raw<T, 4> rdt[NU], rz[NU], rg[NU];
-    StateRows<T, TT, SP> rC;
+    const float bias = a.bias != nullptr ? a.bias[ch] : 0.f;
     const size_t tok0 = static_cast<size_t>(p.b) * a.N;
-    const int ntile = t_end > t_begin ? (t_end - t_begin + TT - 1) / TT : 0;
-    auto fetch = [&](int t0) {
-        const int rows = t_end - t0;
+    const T* dp = static_cast<const T*>(a.dt) + tok0 * a.lddt;
+    const T* zp = static_cast<const T*>(a.z) + tok0 * a.ldz;
+    const T* gp = static_cast<const T*>(a.gy) + tok0 * a.D;
+    const uint32_t lane_at = static_cast<uint32_t>(ch) * sizeof(T);
+    const T* Cp = static_cast<const T*>(a.Cm) + tok0 * a.ldc + p.g * S;
+    const bool gated = a.z != nullptr;
+    auto step = [&](float dt, float g, const WaveRow<T, SP, SCALAR>& C) {
 #pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int r = (tid + k * kScanThreads) / CQ;
-            rdt[k] = rz[k] = rg[k] = Raw<T, 4>{};
-            if (r < rows && r < TT && left > 0) {
-                const size_t t = tok0 + t0 + r;
-                rdt[k] = raw_load_n<T, 4>(static_cast<const T*>(a.dt) + t * a.lddt + uc, left);
-                if (a.z != nullptr) rz[k] = raw_load_n<T, 4>(static_cast<const T*>(a.z) + t * a.ldz + uc, left);
-                rg[k] = raw_load_n<T, 4>(static_cast<const T*>(a.gy) + t * a.D + uc, left);
-            }
-        }
-        rC.load(static_cast<const T*>(a.Cm) + (tok0 + t0) * a.ldc + p.g * a.S, a.ldc, rows, a.S);
+        for (int i = 0; i < SP; ++i) w[i] = exp2_fast(dt * A2[i]) * fmaf(C.get(i), g, w[i]);
     };
-    if (ntile > 0) fetch(t_begin + (ntile - 1) * TT);
-    for (int tile = ntile - 1; tile >= 0; --tile) {
-        const int t0 = t_begin + tile * TT, rows = t_end - t0 < TT ? t_end - t0 : TT;
+    const int blocks = p.t_end > p.t_begin ? (p.t_end - p.t_begin) / kAhead : 0;
+    for (int t = p.t_end - 1; t >= p.t_begin + blocks * kAhead; --t) {
+        WaveRow<T, SP, SCALAR> C;
+        C.load(Cp + static_cast<size_t>(t) * a.ldc, S);
+        const size_t tt = t;
+        float g = up(row_at(gp + tt * a.D, lane_at));
+        if (gated) {
+            const float z = up(row_at(zp + tt * a.ldz, lane_at));
+            g *= z * sigmoid_f(z);
+        }
+        step(step_size(up(row_at(dp + tt * a.lddt, lane_at)) + bias, a.softplus), g, C);
+    }
+    T rdt[kAhead], rz[kAhead] = {}, rg[kAhead];
+    auto fetch = [&](int t0) {
+        const T* dr = dp + t0 * a.lddt;
+        const T* gr = gp + static_cast<size_t>(t0) * a.D;
+        const T* zr = zp + t0 * a.ldz;
 #pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int r = (tid + k * kScanThreads) / CQ;
-            if (UNITS % kScanThreads == 0 || r < TT) {
-                f32v4 d, g;
+        for (int k = 0; k < kAhead; ++k) {
+            rdt[k] = row_at(dr, lane_at);
+            rg[k] = row_at(gr, lane_at);
+            dr += a.lddt;
+            gr += a.D;
+        }
+        if (gated) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    d[i] = r < rows ? step_size(up(rdt[k].v[i]) + bias[i], a.softplus) : 0.f;
-                    g[i] = up(rg[k].v[i]);
-                    if (a.z != nullptr) {
-                        const float z = up(rz[k].v[i]);
-                        g[i] *= z * sigmoid_f(z);
-                    }
-                }
-                *reinterpret_cast<f32v4*>(&sdt[r][4 * cq]) = d;
-                *reinterpret_cast<f32v4*>(&sg[r][4 * cq]) = g;
+            for (int k = 0; k < kAhead; ++k) {
+                rz[k] = row_at(zr, lane_at);
+                zr += a.ldz;
             }
         }
-        rC.store(sC);
-        __syncthreads();
-        if (tile > 0) fetch(t0 - TT);
+    };
+    if (blocks > 0) fetch(p.t_begin + (blocks - 1) * kAhead);
+    for (int blk = blocks - 1; blk >= 0; --blk) {
+        const int t = p.t_begin + blk * kAhead;
+        float dt[kAhead], g[kAhead], z[kAhead];
+        WaveRow<T, SP, SCALAR> C[2];
+        const T* Ct = Cp + static_cast<size_t>(t + kAhead - 1) * a.ldc;
+        C[(kAhead - 1) & 1].load(Ct, S);
 #pragma unroll
-        for (int t = TT - 1; t >= 0; --t) {
-            const float dt = sdt[t][cl], g = sg[t][cl];
-            float Cv[SPL];
-            lds_states<SPL>(sC + t * SP + n0, Cv);
-#pragma unroll
-            for (int i = 0; i < SPL; ++i) w[i] = exp2_fast(dt * A2[i]) * fmaf(Cv[i], g, w[i]);
+        for (int k = 0; k < kAhead; ++k) {
+            dt[k] = up(rdt[k]) + bias;
+            g[k] = up(rg[k]);
+            z[k] = up(rz[k]);
         }
-        __syncthreads();
+        if (blk > 0) fetch(t - kAhead);
+        if (a.softplus) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) dt[k] = softplus_f(dt[k]);
+        }
+        if (gated) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) g[k] *= z[k] * sigmoid_f(z[k]);
+        }
+#pragma unroll
+        for (int k = kAhead - 1; k >= 0; --k) {
+            rows_arrived<SCALAR>();
+            if (k > 0) C[(k - 1) & 1].load(Ct -= a.ldc, S);
+            rows_issued<SCALAR>();
+            step(dt[k], g[k], C[k & 1]);
+        }
     }
     if (!on) return;
     const size_t slot = (static_cast<size_t>(p.b) * pl.nseg + p.seg) * a.D + ch;
-    store_state<SPL>(a.workspace + pl.off_rev + slot * a.S, n0, a.S, w);
+    store_state<SP>(a.workspace + pl.off_rev + slot * S, S, w);
 }
 
 // Entry states (in place of the end states) and, behind each segment, the adjoint (in place
@@ -213,231 +233,382 @@ __global__ __launch_bounds__(kScanThreads) void scan_compose_both_kernel(ScanArg
     float* end = a.workspace + pl.off_end + b * pl.nseg * ds + e;
     float* rev = a.workspace + pl.off_rev + b * pl.nseg * ds + e;
     const float* sum = a.workspace + pl.off_dt + b * pl.nseg * a.D + e / a.S;
+    constexpr int U = 4;           // segments whose loads are in flight together
+    float own[U], dec[U];
     float h = a.state_in != nullptr ? a.state_in[id] : 0.f;
-    for (int s = 0; s < pl.nseg; ++s) {
-        const float own = end[s * ds];
-        end[s * ds] = h;
-        h = fmaf(exp2_fast(A2 * sum[static_cast<size_t>(s) * a.D]), h, own);
+    for (int s0 = 0; s0 < pl.nseg; s0 += U) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int s = s0 + k < pl.nseg ? s0 + k : pl.nseg - 1;
+            own[k] = end[s * ds];
+            dec[k] = exp2_fast(A2 * sum[static_cast<size_t>(s) * a.D]);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (s0 + k >= pl.nseg) break;
+            end[(s0 + k) * ds] = h;
+            h = fmaf(dec[k], h, own[k]);
+        }
     }
     float w = a.gstate_out != nullptr ? a.gstate_out[id] : 0.f;
-    for (int s = pl.nseg - 1; s >= 0; --s) {
-        const float own = s > 0 ? rev[s * ds] : 0.f;
-        rev[s * ds] = w;
-        w = fmaf(exp2_fast(A2 * sum[static_cast<size_t>(s) * a.D]), w, own);
+    for (int s0 = pl.nseg - 1; s0 >= 0; s0 -= U) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int s = s0 - k > 0 ? s0 - k : 0;
+            own[k] = s > 0 ? rev[s * ds] : 0.f;      // the first segment's would go to grad_state_in
+            dec[k] = exp2_fast(A2 * sum[static_cast<size_t>(s) * a.D]);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (s0 - k < 0) break;
+            rev[(s0 - k) * ds] = w;
+            w = fmaf(dec[k], w, own[k]);
+        }
     }
 }
 
-// Sums over a wave's channels (the lanes that share a state group) of v[token][state] for
-// four tokens; afterwards a lane holds token 2 b5 + b4 (its number's bits), and of the SPL
-// states with 16 (8, 4) channels a wave: state 2 b3 + b2 (2 b3 and the one behind it, all).
+// Lanes of the main pass: LPC adjacent lanes hold one channel's states.  With LPC = 4 the state
+// group of a lane is its number's low two bits, flipped in odd channels: then lane ^ 7, which
+// one DPP instruction reaches, is the neighbouring channel's lane of the same state group.
 template <int LPC>
-__device__ __forceinline__ void channel_sum(const float (&v)[4][SPL], int lane, float (&out)[LPC / 4]) {
+__device__ __forceinline__ int state_group(int lane) {
+    const int q = lane & (LPC - 1);
+    return LPC == 4 ? q ^ ((lane & 4) ? 3 : 0) : q;
+}
+// The sum over a channel's LPC lanes, in each of them.
+template <int LPC>
+__device__ __forceinline__ float state_sum(float x) {
+    x += lane_xor<1>(x);
+    x += lane_xor<2>(x);
+    if (LPC >= 8) x += lane_xor<7>(x);
+    if (LPC >= 16) x += lane_xor<8>(x);
+    return x;
+}
+// Sums over a wave's channels (the lanes that share a state group) for four tokens, in steps:
+// tokens 3 and 2 and tokens 1 and 0 are summed over the two halves of the wave as soon as
+// both are there (pair), then all over rows of 16 and down to the channels' last bits (join).
+// Afterwards a lane holds token 2 b4 + b5 (its number's bits), and of the SPL states with 16
+// (8, 4) channels a wave: state 2 b3 + b2 (2 b3 and the one behind it, all).
+__device__ __forceinline__ void channel_pair(const float (&lo)[SPL], const float (&hi)[SPL], float (&r)[SPL]) {
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) r[i] = halves_sum32(lo[i], hi[i]);
+}
+template <int LPC>
+__device__ __forceinline__ void channel_join(const float (&lo)[SPL], const float (&hi)[SPL], float (&out)[LPC / 4]) {
     float r[SPL];
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-        const float lo = halves_sum32(v[0][i], v[2][i]), hi = halves_sum32(v[1][i], v[3][i]);
-        r[i] = halves_sum16(lo, hi);
-    }
+    for (int i = 0; i < SPL; ++i) r[i] = halves_sum16(lo[i], hi[i]);
     if (LPC == 16) {
 #pragma unroll
         for (int i = 0; i < LPC / 4; ++i) out[i] = r[i & 3];
         return;
     }
-    const float s0 = pair_sum<8>(r[0], r[2], lane & 8), s1 = pair_sum<8>(r[1], r[3], lane & 8);
+    const float s0 = pair_sum8(r[0], r[2]), s1 = pair_sum8(r[1], r[3]);
     if (LPC == 8) {
         out[0] = s0;
         out[LPC / 4 - 1] = s1;
     } else {
-        out[0] = pair_sum<7>(s0, s1, lane & 4);
+        out[0] = pair_sum7(s0, s1);
     }
 }
 
-template <typename T, int LPC>
-__global__ __launch_bounds__(kScanThreads, 2) void scan_bwd_kernel(ScanArgs a, ScanPlan pl) {
-    constexpr int CH = kScanThreads / LPC, SP = LPC * SPL, CQ = CH / 4, KEPT = LPC / 4;
-    constexpr int UNITS = kTile * CQ;     // packs of 4 channels of a tile: one a thread at most
-    static_assert(UNITS <= kScanThreads, "one pack a thread");
+// B and C of a tile's tokens, [kTile][SP] in LDS, zeros behind the last state and token.
+template <typename T, int SP>
+struct StateRows {
+    static constexpr int kPer = kTile * SP / kScanThreads;
+    T raw[kPer];
+    // (what lies behind is read from the last token or state there is, and not used)
+    __device__ __forceinline__ void load(const T* p, long long ld, int rows, int S, int tid) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = tid + k * kScanThreads, t = i / SP, n = i % SP;
+            const uint32_t at = static_cast<uint32_t>(t < rows ? t : rows - 1) * static_cast<uint32_t>(ld) + (n < S ? n : S - 1);
+            raw[k] = row_at(p, at * static_cast<uint32_t>(sizeof(T)));
+        }
+    }
+    __device__ __forceinline__ void store(float* lds, int rows, int S, int tid) const {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = tid + k * kScanThreads;
+            lds[i] = i / SP < rows && i % SP < S ? up(raw[k]) : 0.f;
+        }
+    }
+};
+
+// What was read from LDS before is read again behind this point: kept in registers over the
+// parts of a tile it would crowd out the states.
+__device__ __forceinline__ void reload() { asm volatile("" ::: "memory"); }
+
+// A pack at a byte offset from an address that is the same for the whole workgroup; `left` of
+// its elements are there.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ Raw<T, 4> pack_at(const T* base, uint32_t byte, int left) {
+    return raw_load_n<T, 4>(reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + byte), WHOLE ? 4 : left);
+}
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void pack_put(T* base, uint32_t byte, const float (&v)[4], int left) {
+    store_n<T, 4>(reinterpret_cast<T*>(reinterpret_cast<char*>(base) + byte), v, WHOLE ? 4 : left);
+}
+
+// WHOLE: a group's channels and the states are multiples of 4, so that every pack is whole.
+// Idle threads then repeat the loads of others and drop them, which keeps the loads free of
+// branches.
+template <typename T, int LPC, bool WHOLE>
+__global__ __launch_bounds__(kScanThreads, LPC == 16 ? 2 : 3) void scan_bwd_kernel(ScanArgs a, ScanPlan pl) {
+    constexpr int CH = kScanThreads / LPC, SP = LPC * SPL, CQ = CH / 4, KEPT = LPC / 4, ES = sizeof(T);
+    constexpr int PACKS = kTile * CQ;     // packs of 4 channels of a tile: one a thread at most
+    static_assert(PACKS <= kScanThreads && kPart == 4, "one pack a thread, parts of four tokens");
     __shared__ float sdt[kTile][CH], su[kTile][CH], sg[kTile][CH], sdu[kTile][CH], sda[kTile][CH], sy[kTile][CH];
     __shared__ __attribute__((aligned(16))) float sB[kTile * SP], sC[kTile * SP];
     __shared__ float rB[4][kTile * SP], rC[4][kTile * SP];   // each wave's sums over its channels
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const ScanPlace p = scan_place<CH>(a, pl.nblk, pl.nseg, blockIdx.x);
-    const int n = scan_length(a.lengths, p.b, a.N);
-    const int t_begin = p.seg * pl.seg, t_full = t_begin + pl.seg < a.N ? t_begin + pl.seg : a.N;
-    const int t_end = t_full < n ? t_full : n;
-    const int cl = tid / LPC, ch = p.c0 + cl, n0 = state_group<LPC>(lane) * SPL;
-    const bool on = ch < p.cend;
-    const size_t slot = (static_cast<size_t>(p.b) * pl.nseg + p.seg) * a.D + ch;
-    const size_t bd = static_cast<size_t>(p.b) * a.D + ch;
+    __shared__ Raw<T, 4> sx[PACKS], sraw[PACKS], sz[PACKS], sgy[PACKS];   // x, dt, z, gy as they came
+    __shared__ float sbias[CH], sskip[CH];
+    __shared__ f32v4 sgD[PACKS], sgbias[PACKS];               // each pack's sums over tokens
+    const int tid = threadIdx.x, lane = tid & 63;
+    const ScanPlace p = scan_place<CH>(a, pl.nblk, pl.nseg, pl.seg, blockIdx.x);
+    const int cl = tid / LPC, n0 = state_group<LPC>(lane) * SPL;
+    const size_t slot = ((static_cast<size_t>(p.b) * pl.nseg + p.seg) * a.D + p.c0) * a.S;
+    const size_t bd = (static_cast<size_t>(p.b) * a.D + p.c0) * a.S;
     const int tiles = (a.N + kTile - 1) / kTile;
-    float An[SPL], A2[SPL], entry[SPL], w[SPL], gA[SPL];
+    // a lane's SPL of a channel's S states, from the block's first channel
+    struct Lane {
+        int cl, n0, left;          // channel of the block, first state, states from it on (<= 0: none)
+        uint32_t at;               // byte offset in the block's states
+    };
+    auto lane_place = [&]() {
+        const int id = static_cast<int>(opaque(tid)), c = id / LPC, n = state_group<LPC>(id) * SPL;
+        return Lane{c, n, p.c0 + c < p.cend ? a.S - n : 0, (static_cast<uint32_t>(c) * a.S + n) * 4};
+    };
+    auto load_lane = [&](const float* s, float (&v)[SPL]) {
+        const Lane l = lane_place();
+        const Raw<float, SPL> r = pack_at<float, WHOLE>(s, l.left > 0 ? l.at : 0, l.left);
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-        An[i] = on && n0 + i < a.S ? a.A[static_cast<size_t>(ch) * a.S + n0 + i] : 0.f;
-        A2[i] = An[i] * kLog2e;
-        gA[i] = entry[i] = w[i] = 0.f;
-    }
-    if (pl.nseg > 1) {
-        load_state<SPL>(a.workspace + pl.off_end + slot * a.S, n0, a.S, on, entry);
-        load_state<SPL>(a.workspace + pl.off_rev + slot * a.S, n0, a.S, on, w);
-    } else {
-        if (a.state_in != nullptr) load_state<SPL>(a.state_in + bd * a.S, n0, a.S, on, entry);
-        if (a.gstate_out != nullptr) load_state<SPL>(a.gstate_out + bd * a.S, n0, a.S, on, w);
-    }
-    const int cq = tid % CQ, ur = tid / CQ, uc = p.c0 + 4 * cq, left = ur < kTile ? p.cend - uc : 0;
-    float bias[4], skip[4], gD[4] = {}, gbias[4] = {};
+        for (int i = 0; i < SPL; ++i) v[i] = l.left > 0 ? r.v[i] : 0.f;
+    };
+    float A2[SPL], w[SPL] = {}, gA[SPL] = {};
+    load_lane(a.A + static_cast<size_t>(p.c0) * a.S, A2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        bias[i] = a.bias != nullptr && i < left ? a.bias[uc + i] : 0.f;
-        skip[i] = a.Dskip != nullptr && i < left ? a.Dskip[uc + i] : 0.f;
+    for (int i = 0; i < SPL; ++i) A2[i] *= kLog2e;
+    const float* entry = pl.nseg > 1 ? a.workspace + pl.off_end + slot : a.state_in != nullptr ? a.state_in + bd : nullptr;
+    const float* last = pl.nseg > 1 ? a.workspace + pl.off_rev + slot : a.gstate_out != nullptr ? a.gstate_out + bd : nullptr;
+    if (last != nullptr) load_lane(last, w);
+    // This thread's pack of 4 channels of a tile's row: worked out again wherever it is used
+    // (`opaque`), since what is derived from it would otherwise sit in registers throughout.
+    struct Pack {
+        int id, ur, cq, left;      // left: channels from the pack's first one on, <= 0: idle
+        __device__ __forceinline__ uint32_t off(long long ld) const {     // byte offset in the tile, rows ld apart
+            return (static_cast<uint32_t>(ur) * static_cast<uint32_t>(ld) + 4 * cq) * ES;
+        }
+        __device__ __forceinline__ uint32_t from(long long ld, int rows) const {   // the same, of a pack that is there
+            const int r = ur < rows ? ur : 0, c = left > 0 ? 4 * cq : 0;
+            return (static_cast<uint32_t>(r) * static_cast<uint32_t>(ld) + c) * ES;
+        }
+    };
+    auto pack = [&]() {
+        const int id = static_cast<int>(opaque(tid)), ur = id / CQ, cq = id % CQ;
+        return Pack{id, ur, cq, ur < kTile ? p.cend - p.c0 - 4 * cq : 0};
+    };
+    if (tid < PACKS) sgD[tid] = sgbias[tid] = f32v4{0.f, 0.f, 0.f, 0.f};
+    if (tid < CH) {
+        const bool in = p.c0 + tid < p.cend;
+        sbias[tid] = in && a.bias != nullptr ? a.bias[p.c0 + tid] : 0.f;
+        sskip[tid] = in && a.Dskip != nullptr ? a.Dskip[p.c0 + tid] : 0.f;
     }
     const size_t tok0 = static_cast<size_t>(p.b) * a.N;
+    const T* const gy = static_cast<const T*>(a.gy) + p.c0;
+    T* const gx = static_cast<T*>(a.gx) + p.c0;
+    T* const gdt = static_cast<T*>(a.gdt) + p.c0;
+    T* const gz = static_cast<T*>(a.gz) + p.c0;
     // gradient rows behind the sequence's last token are zero
-    for (int t = (t_end > t_begin ? t_end : t_begin) + ur; t < t_full && left > 0; t += kScanThreads / CQ) {
+    const int behind = p.t_end > p.t_begin ? p.t_end : p.t_begin;
+    for (int t0 = behind; t0 < p.t_full; t0 += kTile) {
         const float zero[4] = {};
-        const size_t at = (tok0 + t) * a.D + uc;
-        store_n<T, 4>(static_cast<T*>(a.gx) + at, zero, left);
-        store_n<T, 4>(static_cast<T*>(a.gdt) + at, zero, left);
-        if (a.gz != nullptr) store_n<T, 4>(static_cast<T*>(a.gz) + at, zero, left);
+        const size_t at = (tok0 + t0) * a.D;
+        const Pack k = pack();
+        if (t0 + k.ur >= p.t_full || k.left <= 0) continue;
+        pack_put<T, WHOLE>(gx + at, k.off(a.D), zero, k.left);
+        pack_put<T, WHOLE>(gdt + at, k.off(a.D), zero, k.left);
+        if (a.gz != nullptr) pack_put<T, WHOLE>(gz + at, k.off(a.D), zero, k.left);
     }
-    float* part = a.workspace + pl.off_bc;                 // [2][block][B N][S]
-    const size_t tokens = static_cast<size_t>(a.B) * a.N;
-    const int blk = blockIdx.x % pl.nblk;
-    float* pB = part + (static_cast<size_t>(blk) * tokens + tok0) * a.S;
-    float* pC = pB + static_cast<size_t>(pl.nblk) * tokens * a.S;
-    for (size_t t = static_cast<size_t>(t_end > t_begin ? t_end : t_begin) * a.S + tid; t < static_cast<size_t>(t_full) * a.S;
-         t += kScanThreads)
-        pB[t] = pC[t] = 0.f;
+    const size_t tokens = static_cast<size_t>(a.B) * a.N;   // partial sums [2][block][B N][S]
+    float* const pB = a.workspace + pl.off_bc + (static_cast<size_t>(p.blk) * tokens + tok0) * a.S;
+    float* const pC = pB + static_cast<size_t>(pl.nblk) * tokens * a.S;
+    for (size_t e = static_cast<size_t>(behind) * a.S + tid; e < static_cast<size_t>(p.t_full) * a.S; e += kScanThreads)
+        pB[e] = pC[e] = 0.f;
 
     Raw<T, 4> rx = {}, rdt = {}, rz = {}, rg = {};
-    StateRows<T, kTile, SP> nB, nC;
-    const int ntile = t_end > t_begin ? (t_end - t_begin + kTile - 1) / kTile : 0;
+    StateRows<T, SP> nB, nC;
+    float kept[SPL], cum;
+    const int ntile = p.t_end > p.t_begin ? (p.t_end - p.t_begin + kTile - 1) / kTile : 0;
     auto fetch = [&](int t0) {
-        const int rows = t_end - t0;
-        rx = rdt = rz = rg = Raw<T, 4>{};
-        if (ur < rows && left > 0) {
-            const size_t t = tok0 + t0 + ur;
-            rx = raw_load_n<T, 4>(static_cast<const T*>(a.x) + t * a.ldx + uc, left);
-            rdt = raw_load_n<T, 4>(static_cast<const T*>(a.dt) + t * a.lddt + uc, left);
-            if (a.z != nullptr) rz = raw_load_n<T, 4>(static_cast<const T*>(a.z) + t * a.ldz + uc, left);
-            rg = raw_load_n<T, 4>(static_cast<const T*>(a.gy) + t * a.D + uc, left);
+        const int rows = p.t_end - t0;
+        const size_t t = tok0 + t0;
+        const Pack k = pack();
+        if (WHOLE || (k.ur < rows && k.left > 0)) {
+            rx = pack_at<T, WHOLE>(static_cast<const T*>(a.x) + t * a.ldx + p.c0, k.from(a.ldx, rows), k.left);
+            rdt = pack_at<T, WHOLE>(static_cast<const T*>(a.dt) + t * a.lddt + p.c0, k.from(a.lddt, rows), k.left);
+            if (a.z != nullptr)
+                rz = pack_at<T, WHOLE>(static_cast<const T*>(a.z) + t * a.ldz + p.c0, k.from(a.ldz, rows), k.left);
+            rg = pack_at<T, WHOLE>(gy + t * a.D, k.from(a.D, rows), k.left);
         }
-        nB.load(static_cast<const T*>(a.Bm) + (tok0 + t0) * a.ldb + p.g * a.S, a.ldb, rows, a.S);
-        nC.load(static_cast<const T*>(a.Cm) + (tok0 + t0) * a.ldc + p.g * a.S, a.ldc, rows, a.S);
+        nB.load(static_cast<const T*>(a.Bm) + t * a.ldb + p.g * a.S, a.ldb, rows, a.S, k.id);
+        nC.load(static_cast<const T*>(a.Cm) + t * a.ldc + p.g * a.S, a.ldc, rows, a.S, k.id);
+        const size_t at = (static_cast<size_t>(p.b) * tiles + t0 / kTile) * a.D + p.c0;
+        load_lane(a.workspace + pl.off_ckpt + at * a.S, kept);
+        const Lane l = lane_place();
+        cum = (a.workspace + pl.off_cum + at)[l.left > 0 ? l.cl : 0];
     };
-    if (ntile > 0) fetch(t_begin + (ntile - 1) * kTile);
+    if (ntile > 0) fetch(p.t_begin + (ntile - 1) * kTile);
+    __syncthreads();
     for (int tile = ntile - 1; tile >= 0; --tile) {
-        const int t0 = t_begin + tile * kTile, rows = t_end - t0 < kTile ? t_end - t0 : kTile;
-        // the state in front of the tile
+        const int t0 = p.t_begin + tile * kTile, rows = p.t_end - t0 < kTile ? p.t_end - t0 : kTile;
+        // the state in front of the tile: what its segment made of zero, and what entered it
         float h0[SPL];
-        {
-            const size_t at = (static_cast<size_t>(p.b) * tiles + t0 / kTile) * a.D + ch;
-            load_state<SPL>(a.workspace + pl.off_ckpt + at * a.S, n0, a.S, on, h0);
-            const float cum = on ? a.workspace[pl.off_cum + at] : 0.f;
 #pragma unroll
-            for (int i = 0; i < SPL; ++i) h0[i] = fmaf(exp2_fast(cum * A2[i]), entry[i], h0[i]);
+        for (int i = 0; i < SPL; ++i) h0[i] = kept[i];
+        if (entry != nullptr) {
+            float e[SPL];
+            load_lane(entry, e);
+#pragma unroll
+            for (int i = 0; i < SPL; ++i) h0[i] = fmaf(exp2_fast(cum * A2[i]), e[i], h0[i]);
         }
-        const Raw<T, 4> cx = rx, cz = rz, cg = rg, cdt = rdt;
-        f32v4 d = {0.f, 0.f, 0.f, 0.f}, g = d;
-        if (ur < kTile) {
-            f32v4 u;
+        const Pack k = pack();
+        if (k.ur < kTile) {
+            f32v4 d, u, g;
+            const f32v4 bias = *reinterpret_cast<const f32v4*>(&sbias[4 * k.cq]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                d[i] = ur < rows ? step_size(up(cdt.v[i]) + bias[i], a.softplus) : 0.f;
-                u[i] = d[i] * up(cx.v[i]);
-                g[i] = up(cg.v[i]);
+                const float dt = step_size(up(rdt.v[i]) + bias[i], a.softplus);
+                const bool there = k.ur < rows && i < k.left;
+                float gi = up(rg.v[i]);
                 if (a.z != nullptr) {
-                    const float z = up(cz.v[i]);
-                    g[i] *= z * sigmoid_f(z);
+                    const float z = up(rz.v[i]);
+                    gi *= z * sigmoid_f(z);
                 }
+                d[i] = there ? dt : 0.f;
+                u[i] = there ? dt * up(rx.v[i]) : 0.f;
+                g[i] = there ? gi : 0.f;
             }
-            *reinterpret_cast<f32v4*>(&sdt[ur][4 * cq]) = d;
-            *reinterpret_cast<f32v4*>(&su[ur][4 * cq]) = u;
-            *reinterpret_cast<f32v4*>(&sg[ur][4 * cq]) = g;
+            *reinterpret_cast<f32v4*>(&sdt[k.ur][4 * k.cq]) = d;
+            *reinterpret_cast<f32v4*>(&su[k.ur][4 * k.cq]) = u;
+            *reinterpret_cast<f32v4*>(&sg[k.ur][4 * k.cq]) = g;
+            sx[k.id] = rx;
+            sraw[k.id] = rdt;
+            sz[k.id] = rz;
+            sgy[k.id] = rg;
         }
-        nB.store(sB);
-        nC.store(sC);
+        nB.store(sB, rows, a.S, k.id);
+        nC.store(sC, rows, a.S, k.id);
         __syncthreads();
         if (tile > 0) fetch(t0 - kTile);
-        // forward through the tile: decays and states stay in registers
-        float da[kTile][SPL], hs[kTile][SPL], py[kTile];
+        // the states in front of the tile's parts
+        float hp[kTile / kPart][SPL];
 #pragma unroll
-        for (int t = 0; t < kTile; ++t) {
+        for (int i = 0; i < SPL; ++i) hp[0][i] = h0[i];
+#pragma unroll
+        for (int t = 0; t < kTile - kPart; ++t) {
             const float dt = sdt[t][cl], u = su[t][cl];
-            float Bv[SPL], Cv[SPL];
-            lds_states<SPL>(sB + t * SP + n0, Bv);
-            lds_states<SPL>(sC + t * SP + n0, Cv);
-            py[t] = 0.f;
+            const f32v4 Bv = *reinterpret_cast<const f32v4*>(sB + t * SP + n0);
 #pragma unroll
-            for (int i = 0; i < SPL; ++i) {
-                da[t][i] = exp2_fast(dt * A2[i]);
-                hs[t][i] = fmaf(da[t][i], t > 0 ? hs[t > 0 ? t - 1 : 0][i] : h0[i], u * Bv[i]);
-                py[t] = fmaf(Cv[i], hs[t][i], py[t]);
+            for (int i = 0; i < SPL; ++i) h0[i] = fmaf(exp2_fast(dt * A2[i]), h0[i], u * Bv[i]);
+            if (t % kPart == kPart - 1) {
+#pragma unroll
+                for (int i = 0; i < SPL; ++i) hp[t / kPart + 1][i] = h0[i];
+                reload();
             }
         }
+        float tA[SPL] = {};
 #pragma unroll
-        for (int t = 0; t < kTile; t += LPC) sy[t + (lane & (LPC - 1))][cl] = state_sum<LPC>(py + t, lane);
-        // and back
-        float pu[kTile], pa[kTile], tA[SPL] = {};
+        for (int tb = kTile - kPart; tb >= 0; tb -= kPart) {
+            // forward through the part: its decays and the states before its tokens stay in
+            // registers; y and dC need only what is known here
+            const int id = static_cast<int>(opaque(tid)), row = tb + 2 * ((id >> 4) & 1) + ((id >> 5) & 1);
+            const int s0 = state_group<LPC>(id) * SPL +
+                           (LPC == 16 ? 0 : LPC == 8 ? (id >> 3 & 1) * 2 : (id >> 3 & 1) * 2 + (id >> 2 & 1));
+            float da[kPart][SPL], hs[kPart][SPL], v[2][SPL], c[2][SPL], o[KEPT], h[SPL];
 #pragma unroll
-        for (int tb = kTile - 4; tb >= 0; tb -= 4) {
-            float vB[4][SPL], vC[4][SPL];
+            for (int i = 0; i < SPL; ++i) h[i] = hp[tb / kPart][i];
 #pragma unroll
-            for (int j = 3; j >= 0; --j) {
-                const int t = tb + j;
-                const float dt = sdt[t][cl], u = su[t][cl], gt = sg[t][cl];
-                float Bv[SPL], Cv[SPL];
-                lds_states<SPL>(sB + t * SP + n0, Bv);
-                lds_states<SPL>(sC + t * SP + n0, Cv);
-                pu[t] = pa[t] = 0.f;
+            for (int t = 0; t < kPart; ++t) {
+                const float dt = sdt[tb + t][cl], u = su[tb + t][cl], gt = sg[tb + t][cl];
+                const f32v4 Bv = *reinterpret_cast<const f32v4*>(sB + (tb + t) * SP + n0);
+                const f32v4 Cv = *reinterpret_cast<const f32v4*>(sC + (tb + t) * SP + n0);
+                float y = 0.f;
+#pragma unroll
+                for (int i = 0; i < SPL; ++i) {
+                    hs[t][i] = h[i];
+                    da[t][i] = exp2_fast(dt * A2[i]);
+                    h[i] = fmaf(da[t][i], h[i], u * Bv[i]);
+                    y = fmaf(Cv[i], h[i], y);
+                    v[t & 1][i] = gt * h[i];
+                }
+                y = state_sum<LPC>(y);
+                if ((lane & (LPC - 1)) == 0) sy[tb + t][cl] = y;
+                if (t & 1) channel_pair(v[0], v[1], c[t / 2]);
+            }
+            channel_join<LPC>(c[0], c[1], o);
+#pragma unroll
+            for (int k = 0; k < KEPT; ++k) rC[id >> 6][row * SP + s0 + k] = o[k];
+            // and back
+            reload();
+#pragma unroll
+            for (int t = kPart - 1; t >= 0; --t) {
+                const float dt = sdt[tb + t][cl], u = su[tb + t][cl], gt = sg[tb + t][cl];
+                const f32v4 Bv = *reinterpret_cast<const f32v4*>(sB + (tb + t) * SP + n0);
+                const f32v4 Cv = *reinterpret_cast<const f32v4*>(sC + (tb + t) * SP + n0);
+                float du = 0.f, dA = 0.f;
 #pragma unroll
                 for (int i = 0; i < SPL; ++i) {
                     const float adj = fmaf(Cv[i], gt, w[i]);
-                    pu[t] = fmaf(adj, Bv[i], pu[t]);
-                    vB[j][i] = adj * u;
-                    vC[j][i] = gt * hs[t][i];
+                    du = fmaf(adj, Bv[i], du);
+                    v[t & 1][i] = adj * u;
                     w[i] = adj * da[t][i];
-                    const float q = w[i] * (t > 0 ? hs[t > 0 ? t - 1 : 0][i] : h0[i]);
-                    pa[t] = fmaf(An[i], q, pa[t]);
+                    const float q = w[i] * hs[t][i];
+                    dA = fmaf(A2[i], q, dA);
                     tA[i] = fmaf(dt, q, tA[i]);
                 }
+                du = state_sum<LPC>(du);
+                dA = state_sum<LPC>(dA);
+                if ((lane & (LPC - 1)) == 0) {
+                    sdu[tb + t][cl] = du;
+                    sda[tb + t][cl] = dA;
+                }
+                if (t % 2 == 0) channel_pair(v[0], v[1], c[t / 2]);
             }
-            float oB[KEPT], oC[KEPT];
-            channel_sum<LPC>(vB, lane, oB);
-            channel_sum<LPC>(vC, lane, oC);
-            const int t = tb + 2 * (lane >> 5) + ((lane >> 4) & 1);
-            const int s0 = n0 + (LPC == 16 ? 0 : LPC == 8 ? ((lane >> 3) & 1) * 2 : ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1));
+            channel_join<LPC>(c[0], c[1], o);
 #pragma unroll
-            for (int k = 0; k < KEPT; ++k) {
-                rB[wave][t * SP + s0 + k] = oB[k];
-                rC[wave][t * SP + s0 + k] = oC[k];
-            }
+            for (int k = 0; k < KEPT; ++k) rB[id >> 6][row * SP + s0 + k] = o[k];
+            reload();
         }
 #pragma unroll
         for (int i = 0; i < SPL; ++i) gA[i] += tA[i];
-#pragma unroll
-        for (int t = 0; t < kTile; t += LPC) {
-            sdu[t + (lane & (LPC - 1))][cl] = state_sum<LPC>(pu + t, lane);
-            sda[t + (lane & (LPC - 1))][cl] = state_sum<LPC>(pa + t, lane);
-        }
         __syncthreads();
-        for (int e = tid; e < rows * SP; e += kScanThreads) {
+        const Pack k2 = pack();
+        for (int e = k2.id; e < rows * SP; e += kScanThreads) {
             const int t = e / SP, s = e % SP;
             if (s >= a.S) continue;
-            const size_t at = static_cast<size_t>(t0 + t) * a.S + s;
-            pB[at] = (rB[0][e] + rB[1][e]) + (rB[2][e] + rB[3][e]);
-            pC[at] = (rC[0][e] + rC[1][e]) + (rC[2][e] + rC[3][e]);
+            float* const rowB = pB + static_cast<size_t>(t0) * a.S;
+            float* const rowC = pC + static_cast<size_t>(t0) * a.S;
+            const uint32_t at = static_cast<uint32_t>(t * a.S + s);
+            rowB[at] = (rB[0][e] + rB[1][e]) + (rB[2][e] + rB[3][e]);
+            rowC[at] = (rC[0][e] + rC[1][e]) + (rC[2][e] + rC[3][e]);
         }
-        if (ur < rows && left > 0) {
-            const f32v4 du = *reinterpret_cast<const f32v4*>(&sdu[ur][4 * cq]);
-            const f32v4 dA = *reinterpret_cast<const f32v4*>(&sda[ur][4 * cq]);
-            const f32v4 ys = *reinterpret_cast<const f32v4*>(&sy[ur][4 * cq]);
+        if (k2.ur < rows && k2.left > 0) {
+            const f32v4 du = *reinterpret_cast<const f32v4*>(&sdu[k2.ur][4 * k2.cq]);
+            const f32v4 dA = *reinterpret_cast<const f32v4*>(&sda[k2.ur][4 * k2.cq]);
+            const f32v4 ys = *reinterpret_cast<const f32v4*>(&sy[k2.ur][4 * k2.cq]);
+            const f32v4 d = *reinterpret_cast<const f32v4*>(&sdt[k2.ur][4 * k2.cq]);
+            const f32v4 g = *reinterpret_cast<const f32v4*>(&sg[k2.ur][4 * k2.cq]);
+            const f32v4 bias = *reinterpret_cast<const f32v4*>(&sbias[4 * k2.cq]);
+            const f32v4 skip = *reinterpret_cast<const f32v4*>(&sskip[4 * k2.cq]);
+            const Raw<T, 4> cx = sx[k2.id], cdt = sraw[k2.id], cz = sz[k2.id], cg = sgy[k2.id];
+            f32v4 gD = sgD[k2.id], gbias = sgbias[k2.id];
             float ox[4], odt[4], oz[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float x = up(cx.v[i]);
                 ox[i] = fmaf(du[i], d[i], g[i] * skip[i]);
-                odt[i] = fmaf(du[i], x, dA[i]);
+                odt[i] = fmaf(du[i], x, dA[i] * (1.f / kLog2e));     // summed with A log2(e)
                 if (a.softplus) odt[i] *= sigmoid_f(up(cdt.v[i]) + bias[i]);
                 gD[i] = fmaf(g[i], x, gD[i]);
                 gbias[i] += odt[i];
@@ -446,35 +617,30 @@ __global__ __launch_bounds__(kScanThreads, 2) void scan_bwd_kernel(ScanArgs a, S
                     oz[i] = up(cg.v[i]) * fmaf(skip[i], x, ys[i]) * fmaf(z * s, 1.f - s, s);
                 }
             }
-            const size_t at = (tok0 + t0 + ur) * a.D + uc;
-            store_n<T, 4>(static_cast<T*>(a.gx) + at, ox, left);
-            store_n<T, 4>(static_cast<T*>(a.gdt) + at, odt, left);
-            if (a.gz != nullptr) store_n<T, 4>(static_cast<T*>(a.gz) + at, oz, left);
+            sgD[k2.id] = gD;
+            sgbias[k2.id] = gbias;
+            const size_t at = (tok0 + t0) * a.D;
+            pack_put<T, WHOLE>(gx + at, k2.off(a.D), ox, k2.left);
+            pack_put<T, WHOLE>(gdt + at, k2.off(a.D), odt, k2.left);
+            if (a.gz != nullptr) pack_put<T, WHOLE>(gz + at, k2.off(a.D), oz, k2.left);
         }
     }
     // [B nseg][S + 2][D] partial sums of the parameters' gradients
-    float* par = a.workspace + pl.off_par + static_cast<size_t>(blockIdx.x / pl.nblk) * (a.S + 2) * a.D;
-    if (on) {
+    float* const par = a.workspace + pl.off_par + static_cast<size_t>(blockIdx.x / pl.nblk) * (a.S + 2) * a.D;
+    const Lane l = lane_place();
+    if (l.left > 0) {
 #pragma unroll
         for (int i = 0; i < SPL; ++i)
-            if (n0 + i < a.S) par[static_cast<size_t>(n0 + i) * a.D + ch] = gA[i];
-        if (p.seg == 0 && a.gstate_in != nullptr) store_state<SPL>(a.gstate_in + bd * a.S, n0, a.S, w);
-    }
-    __syncthreads();
-    if (ur < kTile) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sdu[ur][4 * cq + i] = gD[i];
-            sda[ur][4 * cq + i] = gbias[i];
-        }
+            if (i < l.left) par[static_cast<size_t>(l.n0 + i) * a.D + p.c0 + l.cl] = gA[i];
+        if (p.seg == 0 && a.gstate_in != nullptr) pack_put<float, WHOLE>(a.gstate_in + bd, l.at, w, l.left);
     }
     __syncthreads();
     if (tid < CH && p.c0 + tid < p.cend) {
         float s = 0.f, b = 0.f;
 #pragma unroll
         for (int r = 0; r < kTile; ++r) {
-            s += sdu[r][tid];
-            b += sda[r][tid];
+            s += sgD[r * CQ + tid / 4][tid % 4];
+            b += sgbias[r * CQ + tid / 4][tid % 4];
         }
         par[static_cast<size_t>(a.S) * a.D + p.c0 + tid] = s;
         par[static_cast<size_t>(a.S + 1) * a.D + p.c0 + tid] = b;
@@ -496,25 +662,36 @@ __global__ __launch_bounds__(kScanThreads) void scan_bc_kernel(ScanArgs a, ScanP
     static_cast<T*>(id < one ? a.gB : a.gC)[e] = down<T>(t);
 }
 
-template <typename T, int LPC>
-hipError_t bwd_cfg(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
+template <typename T, int SP, bool SCALAR>
+hipError_t first_passes(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
+    const dim3 block(kScanThreads);
+    constexpr unsigned wpg = kScanThreads / 64;
+    const unsigned waves = static_cast<unsigned>(a.G * ((a.D / a.G + 63) / 64)) * a.B;
+    ProfScope prof(kProfScanPre, st);
+    hipLaunchKernelGGL((scan_keep_kernel<T, SP, SCALAR>), dim3((waves * p.nseg + wpg - 1) / wpg), block, 0, st, a, p);
+    if (p.nseg > 1) {
+        hipLaunchKernelGGL((scan_rev_kernel<T, SP, SCALAR>), dim3((waves * (p.nseg - 1) + wpg - 1) / wpg), block, 0, st, a, p);
+        const size_t n = static_cast<size_t>(a.B) * a.D * a.S;
+        hipLaunchKernelGGL(scan_compose_both_kernel, dim3(static_cast<unsigned>((n + kScanThreads - 1) / kScanThreads)), block,
+                           0, st, a, p);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int SP>
+hipError_t bwd_states(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
+    constexpr int LPC = SP <= 16 ? 4 : SP / 4;
     const dim3 block(kScanThreads);
     const unsigned wgs = static_cast<unsigned>(p.nblk) * a.B;
     if (wgs > 0) {
-        {
-            ProfScope prof(kProfScanPre, st);
-            hipLaunchKernelGGL((scan_keep_kernel<T, LPC>), dim3(wgs * p.nseg), block, 0, st, a, p);
-        }
-        if (p.nseg > 1) {
-            ProfScope prof(kProfScanPre, st);
-            hipLaunchKernelGGL((scan_rev_kernel<T, LPC>), dim3(wgs * (p.nseg - 1)), block, 0, st, a, p);
-            const size_t n = static_cast<size_t>(a.B) * a.D * a.S;
-            hipLaunchKernelGGL(scan_compose_both_kernel, dim3(static_cast<unsigned>((n + kScanThreads - 1) / kScanThreads)),
-                               block, 0, st, a, p);
-        }
+        hipError_t e = scalar_rows(a, SP) ? first_passes<T, SP, true>(a, p, st) : first_passes<T, SP, false>(a, p, st);
+        if (e != hipSuccess) return e;
         {
             ProfScope prof(kProfSelScan, st);
-            hipLaunchKernelGGL((scan_bwd_kernel<T, LPC>), dim3(wgs * p.nseg), block, 0, st, a, p);
+            if (a.D / a.G % 4 == 0 && a.S % 4 == 0)
+                hipLaunchKernelGGL((scan_bwd_kernel<T, LPC, true>), dim3(wgs * p.nseg), block, 0, st, a, p);
+            else
+                hipLaunchKernelGGL((scan_bwd_kernel<T, LPC, false>), dim3(wgs * p.nseg), block, 0, st, a, p);
         }
         const size_t n = 2 * static_cast<size_t>(a.B) * a.N * a.G * a.S;
         if (n > 0) {
@@ -522,7 +699,7 @@ hipError_t bwd_cfg(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
             hipLaunchKernelGGL((scan_bc_kernel<T>), dim3(static_cast<unsigned>((n + kScanThreads - 1) / kScanThreads)), block,
                                0, st, a, p);
         }
-        const hipError_t e = hipGetLastError();
+        e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     const ColReduceArgs c{a.workspace + p.off_par, a.B * p.nseg, a.S + 2, a.S, a.D, a.gA, a.gD, a.gbias, false};
@@ -531,24 +708,24 @@ hipError_t bwd_cfg(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
 
 template <typename T>
 hipError_t bwd_typed(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
-    return p.cfg == 0 ? bwd_cfg<T, 4>(a, p, st) : p.cfg == 1 ? bwd_cfg<T, 8>(a, p, st) : bwd_cfg<T, 16>(a, p, st);
+    if (a.S <= 16) return bwd_states<T, 16>(a, p, st);
+    return a.S <= 32 ? bwd_states<T, 32>(a, p, st) : bwd_states<T, 64>(a, p, st);
 }
 
 }  // namespace
 
 ScanPlan scan_bwd_plan(int B, int N, int D, int G, int S) {
     ScanPlan p{};
-    p.cfg = S <= 16 ? 0 : S <= 32 ? 1 : 2;
-    p.ch = p.cfg == 0 ? 64 : p.cfg == 1 ? 32 : 16;
-    p.nblk = G * ((D / G + p.ch - 1) / p.ch);
-    const size_t wgs = static_cast<size_t>(p.nblk) * (B > 0 ? B : 1);
-    // Segments: as many as bring the chip two workgroups a CU, of 8 tiles at least.
-    const int most = N / (8 * kTile) > 1 ? N / (8 * kTile) : 1;
-    int want = wgs >= 256 ? 1 : static_cast<int>((512 + wgs - 1) / wgs);
+    const int ch = S <= 16 ? 64 : S <= 32 ? 32 : 16;       // channels of a workgroup of the main pass
+    p.nblk = G * ((D / G + ch - 1) / ch);
+    // Segments: as many as bring the chip four waves of the first passes a SIMD, of 4 tiles at
+    // least.
+    const size_t waves = static_cast<size_t>(G) * ((D / G + 63) / 64) * (B > 0 ? B : 1);
+    const int most = N / (4 * kTile) > 1 ? N / (4 * kTile) : 1;
+    int want = waves >= 2048 ? 1 : static_cast<int>((kWantWaves + waves - 1) / waves);
     if (want > most) want = most;
-    const int steps = (N + 2 * kTile - 1) / (2 * kTile);   // the first passes take two tiles a step
-    const int per = (steps + want - 1) / want;
-    p.seg = per > 0 ? per * 2 * kTile : 2 * kTile;
+    const int steps = (N + kTile - 1) / kTile, per = (steps + want - 1) / want;
+    p.seg = per > 0 ? per * kTile : kTile;
     p.nseg = N > 0 ? (N - 1) / p.seg + 1 : 1;
     const size_t bs = static_cast<size_t>(B) * p.nseg * D, tiles = (static_cast<size_t>(N) + kTile - 1) / kTile;
     size_t at = 0;

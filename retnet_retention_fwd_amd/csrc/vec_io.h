@@ -60,21 +60,15 @@ __device__ __forceinline__ void store_n(T* p, const float* x, int left) {
 template <typename T>
 constexpr int kPack = 16 / static_cast<int>(sizeof(T));   // elements of a 16-byte access
 
-// e^x to a few units in the last place: the rounding of x log2(e) is carried along (alone
-// it costs |x| 2^-24).  Results under the normal range may flush to zero.
-__device__ __forceinline__ float exp_acc(float x) {
-    x = x < -126.f ? -126.f : x;
-    const float t = x * 1.44269502162933349609f;                 // log2(e), upper part
-    const float lo = fmaf(x, 1.44269502162933349609f, -t) + x * 1.92596299112661746887e-8f;
-    const float e = __builtin_amdgcn_exp2f(t);
-    return fmaf(e, lo * 0.693147180559945f, e);
-}
 __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
-__device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + exp_acc(x < -80.f ? 80.f : -x)); }
+// 1 / (1 + e^-x).  The exponent's rounding is relative to x (|x| 2^-24 of e^-x), which the
+// bounded x of a gate keeps near the rounding of its own type.
+__device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + __builtin_amdgcn_exp2f(x * -kLog2e)); }
 // log(1 + e^x), x itself above 20 (the difference there is below half a unit of x).  The
-// logarithm of w = 1 + e is divided by (w - 1) / e, which takes out the rounding of w.
+// logarithm of w = 1 + e is divided by (w - 1) / e, which takes out the rounding of w: small
+// e would lose all of its digits there.
 __device__ __forceinline__ float softplus_f(float x) {
-    const float e = exp_acc(x > 20.f ? 20.f : x);
+    const float e = __builtin_amdgcn_exp2f((x > 20.f ? 20.f : x) * kLog2e);
     const float w = 1.f + e, d = w - 1.f;
     const float l = d > 0.f ? __builtin_amdgcn_logf(w) * 0.693147180559945f * (e * rcp(d)) : e;
     return x <= 20.f ? l : x;
@@ -99,11 +93,27 @@ __device__ __forceinline__ float halves_sum16(float a, float b) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// The sum over two partner lanes, kept as a where the lane's bit is clear, as b where set.
-template <int MASK>
-__device__ __forceinline__ float pair_sum(float a, float b, bool bit) {
-    const float keep = bit ? b : a, send = bit ? a : b;
-    return keep + lane_xor<MASK>(send);
+// Sums over partner lanes that differ in bit 3 (lane ^ 8) or, mirrored, in bit 2 (lane ^ 7):
+// of a where the bit is clear, of b where it is set.  The second addition writes only the
+// banks (four lanes) with the bit set, which takes the place of two selects; the leading
+// wait covers the two slots between writing a register and reading it across lanes.
+__device__ __forceinline__ float pair_sum8(float a, float b) {
+    float r;
+    asm("s_nop 1\n\t"
+        "v_add_f32_dpp %0, %1, %1 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %0, %2, %2 row_ror:8 row_mask:0xf bank_mask:0xc"
+        : "=&v"(r)
+        : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ float pair_sum7(float a, float b) {
+    float r;
+    asm("s_nop 1\n\t"
+        "v_add_f32_dpp %0, %1, %1 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %0, %2, %2 row_half_mirror row_mask:0xf bank_mask:0xa"
+        : "=&v"(r)
+        : "v"(a), "v"(b));
+    return r;
 }
 // The sum over a wave's 64 lanes, in every lane.
 __device__ __forceinline__ float wave_sum(float x) {

@@ -194,12 +194,14 @@ def test_step_continues_a_prompt(B, D, G, S, dtype):
 
 
 def test_state_in_place_and_split():
-    """A prompt in two parts with the state updated in place is the whole prompt, bit for bit
-    where the parts end at tiles of one segment."""
+    """A prompt in two parts, the state updated in place, against the whole sequence's recurrence.
+    (Not bit for bit against one call: a sequence may be cut into segments that the parts are
+    not, and a segment's entry state is composed, which rounds in another order.)"""
     print("\n[case] scan in place", flush=True)
     t, v = case(2, 128, 70, 1, 16, "bf16", False, 500)
     kw = dict(D=t["D"], dt_bias=t["dt_bias"], softplus=True)
-    y, h = R().selective_scan_fwd(*fwd_args(t), z=t["z"], state_in=t["state_in"], return_state=True, **kw)
+    ry, rh = O.selective_scan(*fwd_args(v), v["D"], v["z"], v["dt_bias"], True, v["state_in"])
+    my, mh = mags(v, True)
     state, ys = t["state_in"].clone(), []
     for lo in (0, 64):
         p = {m: t[m][:, lo:lo + 64].contiguous() for m in ("x", "dt", "z", "Bm", "Cm")}
@@ -207,7 +209,9 @@ def test_state_in_place_and_split():
                                      **kw)
         ys.append(got[0])
         assert got[1] is state
-    assert torch.equal(torch.cat(ys, 1), y) and torch.equal(state, h)
+    k = 8 * 128 + 4 * 16 + 64
+    check(torch.cat(ys, 1), ry, my, k, "y")
+    check(state, rh, mh, k, "state")
     # segmented, in place: the entry states are composed before any state is written
     t, v = case(1, 700, 12, 1, 16, "f32", False, 510)
     kw = dict(D=t["D"], dt_bias=t["dt_bias"], softplus=True)
