@@ -13,7 +13,7 @@ import contextlib
 import ctypes
 import math
 
-from ._lib import _check, _dtype_code, _ptr, _require, _torch, lib
+from ._lib import RETN_BF16, RETN_F32, _check, _dtype_code, _require, lib
 
 _vp, _i, _ll, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
 
@@ -36,39 +36,59 @@ SIGNATURES = {
     "selective_scan_step": [_vp] * 10 + [_ll] * 5 + [_i] * 6 + [_vp],
 }
 
-_bound = None
+_Strides = _ll * 12
+_bound = {}
+_HERE = contextlib.nullcontext()
+_T = None
+
+
+def _torch():
+    """torch, imported by the first call (importing the package does not)."""
+    global _T
+    if _T is None:
+        import torch
+        _T = torch
+    return _T
 
 
 def _fn(name):
-    """The library's function, its argument types set once."""
-    global _bound
-    if _bound is None:
-        L = lib()
-        got = {}
-        for n, types in SIGNATURES.items():
-            f = getattr(L, n)
-            f.argtypes = types
-            f.restype = _sz if n.endswith("_bytes") else _i
-            got[n] = f
-        _bound = got
-    return _bound[name]
+    """The library's function with its argument types, looked up once."""
+    f = _bound.get(name)
+    if f is None:
+        f = getattr(lib(), name)
+        f.argtypes = SIGNATURES[name]
+        f.restype = _sz if name.endswith("_bytes") else _i
+        _bound[name] = f
+    return f
 
 
-@contextlib.contextmanager
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _on(dev, stream):
-    """Makes the tensors' device current and allocations belong to the stream the kernels
-    run on; gives that stream's handle."""
+    """A context in which the tensors' device is current and allocations belong to the stream
+    that the kernels run on, and that stream's handle.  The current stream of the current
+    device needs no context."""
     torch = _torch()
-    with contextlib.ExitStack() as stack:
-        if torch.cuda.current_device() != dev.index:
-            stack.enter_context(torch.cuda.device(dev))
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-            stack.enter_context(torch.cuda.stream(stream))
-        else:
-            stream = torch.cuda.current_stream()
-        yield ctypes.c_void_p(stream.cuda_stream)
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return _HERE, torch._C._cuda_getCurrentRawStream(dev.index)
+    stack = contextlib.ExitStack()
+    if torch.cuda.current_device() != dev.index:
+        stack.enter_context(torch.cuda.device(dev))
+    if stream is None:
+        return stack, torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream.device != dev:
+        stack.close()
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    stack.enter_context(torch.cuda.stream(stream))
+    return stack, stream.cuda_stream
+
+
+def _code(t):
+    """Type code of the activations."""
+    torch = _torch()
+    return RETN_BF16 if t.dtype is torch.bfloat16 else RETN_F32 if t.dtype is torch.float32 else _dtype_code(t)
 
 
 def _shape(t, name, shape):
@@ -76,16 +96,32 @@ def _shape(t, name, shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _dense(t, name, dtype, dev, shape):
+    """A contiguous tensor of this type, device and shape."""
+    try:       # what holds as a rule, at the price of four attributes
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _require(t, name, dtype, dev)
+    _shape(t, name, shape)
+
+
 def _given(t, name, dtype, dev, shape):
     """An optional contiguous tensor of this type and shape."""
     if t is not None:
-        _require(t, name, dtype, dev)
-        _shape(t, name, shape)
+        _dense(t, name, dtype, dev, shape)
 
 
 def _rows(t, name, dtype, dev, shape, inner=1):
     """A [B, N, ...] (or [B, ...]) tensor whose tokens lie one stride apart; its `inner` last
     axes are contiguous.  Returns that stride."""
+    if dev is not None:
+        try:
+            if t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
+                return shape[-1] if inner == 1 else shape[-1] * shape[-2]
+        except AttributeError:
+            pass
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -95,24 +131,26 @@ def _rows(t, name, dtype, dev, shape, inner=1):
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None:
+    size, step = t.shape, t.stride()
+    if shape is not None and size != shape:
         _shape(t, name, shape)
     width = 1
     for i in range(1, inner + 1):
-        if t.shape[-i] != 1 and t.stride(-i) != width:
+        if step[-i] != width and size[-i] != 1:
             raise ValueError(f"{name}: the elements of a token must be contiguous")
-        width *= t.shape[-i]
-    lead = t.dim() - inner
-    if lead == 1:
-        ld = t.stride(0) if t.shape[0] > 1 else width
+        width *= size[-i]
+    if len(size) - inner == 1:
+        ld = step[0] if size[0] > 1 else width
     else:
-        B, N = t.shape[0], t.shape[1]
-        ld = t.stride(1) if N > 1 else t.stride(0) if B > 1 else width
-        if B > 1 and N > 1 and t.stride(0) != N * ld:
+        B, N = size[0], size[1]
+        ld = step[1] if N > 1 else step[0] if B > 1 else width
+        if B > 1 and N > 1 and step[0] != N * ld:
             raise ValueError(f"{name}: tokens must lie one stride apart over the whole batch")
-    if t.numel() > 0 and ld < width:
-        raise ValueError(f"{name}: tokens overlap")
-    return max(ld, width)
+    if ld < width:
+        if t.numel() > 0:
+            raise ValueError(f"{name}: tokens overlap")
+        return width
+    return ld
 
 
 def _weights(w, b, x, w_shape, D):
@@ -120,12 +158,12 @@ def _weights(w, b, x, w_shape, D):
     torch = _torch()
     first = w if w is not None else b
     if first is None:
-        return 0
+        return RETN_F32
     if first.dtype not in (torch.float32, x.dtype):
         raise TypeError(f"weight and bias must be float32 or {x.dtype}, got {first.dtype}")
     _given(w, "weight", first.dtype, x.device, w_shape)
     _given(b, "bias", first.dtype, x.device, (D,))
-    return _dtype_code(first)
+    return _code(first)
 
 
 def _space(need, workspace, dev):
@@ -156,8 +194,9 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, return_stats=False, out=
     D, dev = x.shape[-1], x.device
     rows = x.numel() // D
     wcode = _weights(weight, bias, x, (D,), D)
-    code = _dtype_code(x)
-    with _on(dev, stream) as s:
+    code = _code(x)
+    on, s = _on(dev, stream)
+    with on:
         _given(out, "out", x.dtype, dev, x.shape)
         y = torch.empty_like(x) if out is None else out
         mean = rstd = None
@@ -177,13 +216,14 @@ def layer_norm_bwd(x, weight, mean, rstd, grad_y, bias_grad=True, weight_grad=Tr
         raise ValueError("x must be [..., D] with D >= 1")
     D, dev = x.shape[-1], x.device
     rows = x.numel() // D
-    _given(grad_y, "grad_y", x.dtype, dev, x.shape)
-    _given(mean, "mean", torch.float32, dev, x.shape[:-1])
-    _given(rstd, "rstd", torch.float32, dev, x.shape[:-1])
+    _dense(grad_y, "grad_y", x.dtype, dev, x.shape)
+    _dense(mean, "mean", torch.float32, dev, x.shape[:-1])
+    _dense(rstd, "rstd", torch.float32, dev, x.shape[:-1])
     wcode = _weights(weight, None, x, (D,), D)
     wt = torch.float32 if weight is None else weight.dtype
-    code = _dtype_code(x)
-    with _on(dev, stream) as s:
+    code = _code(x)
+    on, s = _on(dev, stream)
+    with on:
         gx = torch.empty_like(x)
         gw = torch.empty(D, dtype=wt, device=dev) if weight is not None and weight_grad else None
         gb = torch.empty(D, dtype=wt, device=dev) if bias_grad else None
@@ -242,7 +282,8 @@ def rotary_table(freq, count, first=0, magnitude=1.0, device=None, stream=None):
         dev = freq.device
     elif dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    with _on(dev, stream) as s:
+    on, s = _on(dev, stream)
+    with on:
         f = freq.to(dev).contiguous()
         table = torch.empty((count, f.numel(), 2), dtype=torch.float32, device=dev)
         _check(_fn("rotary_table")(_ptr(table), _ptr(f), f.numel(), int(first), int(count), float(magnitude), s),
@@ -250,53 +291,61 @@ def rotary_table(freq, count, first=0, magnitude=1.0, device=None, stream=None):
     return table
 
 
-def _heads(t, name, like, shape):
+def _heads(t, name, dtype, dev, shape):
+    """Strides of a [B,H,N,d] tensor with adjacent head elements."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dim() != 4:
         raise ValueError(f"{name} must be [B,H,N,d]")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise TypeError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    if shape is not None:
+    if dtype is not None and (t.dtype is not dtype or t.get_device() != dev.index):
+        raise TypeError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
+    if shape is not None and t.shape != shape:
         _shape(t, name, shape)
-    if t.shape[-1] != 1 and t.stride(-1) != 1:
+    step = t.stride()
+    if step[3] != 1 and t.shape[3] != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return t.stride()[:3]
+    return step[:3]
 
 
 def _rotary(fn, q, k, table, positions, offset, interleaved, q_scale, k_scale, out_q, out_k, stream):
     torch = _torch()
-    sq = _heads(q, "q", None, None)
+    sq = _heads(q, "q", None, None, None)
     B, Hq, N, d = q.shape
-    dev, code = q.device, _dtype_code(q)
-    _require(table, "table", torch.float32, dev)
-    if table.dim() != 3 or table.shape[2] != 2:
+    dev, t, code = q.device, q.dtype, _code(q)
+    if not isinstance(table, torch.Tensor) or table.dim() != 3 or table.shape[2] != 2:
         raise ValueError("table must be [positions, rot/2, 2]")
-    sk, Hk = (0, 0, 0), 0
+    far, half, _ = table.shape
+    _dense(table, "table", torch.float32, dev, (far, half, 2))
+    sk = sok = (0, 0, 0)
+    Hk = pk = pok = 0
     if k is not None:
-        sk = _heads(k, "k", q, None)
-        Hk = k.shape[1]
-        if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d:
+        sk = _heads(k, "k", t, dev, None)
+        Hk, pk = k.shape[1], k.data_ptr()
+        if k.shape != (B, Hk, N, d):
             raise ValueError(f"k must be [{B}, Hk, {N}, {d}], got {list(k.shape)}")
-    batched = 0
+    batched, pp = 0, None
     if positions is not None:
-        _require(positions, "positions", torch.int64, dev)
-        batched = int(positions.dim() == 2)
-        _shape(positions, "positions", (B, N) if batched else (N,))
-    with _on(dev, stream) as s:
+        batched, pp = int(positions.dim() == 2), positions.data_ptr()
+        _dense(positions, "positions", torch.int64, dev, (B, N) if batched else (N,))
+    on, s = _on(dev, stream)
+    with on:
         if out_q is None:
-            out_q = torch.empty((B, Hq, N, d), dtype=q.dtype, device=dev)
-        if out_k is None and k is not None:
-            out_k = torch.empty((B, Hk, N, d), dtype=q.dtype, device=dev)
-        soq = _heads(out_q, "out_q", q, q.shape)
-        sok = _heads(out_k, "out_k", q, k.shape) if k is not None else (0, 0, 0)
-        strides = (_ll * 12)(*sq, *soq, *sk, *sok)
-        _check(_fn(fn)(_ptr(q), _ptr(k), _ptr(out_q), _ptr(out_k) if k is not None else None, strides, _ptr(table),
-                       table.shape[0], _ptr(positions), batched, int(offset), B, Hq, Hk, N, d, 2 * table.shape[1],
-                       int(bool(interleaved)), float(q_scale), float(k_scale), code, s), fn)
+            out_q = torch.empty((B, Hq, N, d), dtype=t, device=dev)
+            soq = (Hq * N * d, N * d, d)
+        else:
+            soq = _heads(out_q, "out_q", t, dev, q.shape)
+        if k is not None:
+            if out_k is None:
+                out_k = torch.empty((B, Hk, N, d), dtype=t, device=dev)
+                sok = (Hk * N * d, N * d, d)
+            else:
+                sok = _heads(out_k, "out_k", t, dev, k.shape)
+            pok = out_k.data_ptr()
+        _check(_fn(fn)(q.data_ptr(), pk, out_q.data_ptr(), pok, _Strides(*sq, *soq, *sk, *sok), table.data_ptr(), far, pp,
+                       batched, offset, B, Hq, Hk, N, d, 2 * half, 1 if interleaved else 0, q_scale, k_scale, code, s), fn)
     return out_q if k is None else (out_q, out_k)
 
 
@@ -336,10 +385,11 @@ def causal_conv_fwd(x, weight, bias=None, silu=False, state_in=None, return_stat
     sequence of a padded batch.  Returns y, or (y, state_out)."""
     torch = _torch()
     ldx, D, K, wcode = _conv_shapes(x, weight, bias, 3)
-    B, N, dev, code = x.shape[0], x.shape[1], x.device, _dtype_code(x)
+    B, N, dev, code = x.shape[0], x.shape[1], x.device, _code(x)
     _given(state_in, "state_in", x.dtype, dev, (B, K - 1, D))
     _lengths(lengths, dev, B)
-    with _on(dev, stream) as s:
+    on, s = _on(dev, stream)
+    with on:
         _given(out, "out", x.dtype, dev, (B, N, D))
         _given(state_out, "state_out", x.dtype, dev, (B, K - 1, D))
         y = torch.empty((B, N, D), dtype=x.dtype, device=dev) if out is None else out
@@ -356,13 +406,13 @@ def causal_conv_bwd(x, weight, grad_y, bias=None, silu=False, state_in=None, gra
     return_grad_state_in is set; grad_bias is None without a bias."""
     torch = _torch()
     ldx, D, K, wcode = _conv_shapes(x, weight, bias, 3)
-    B, N, dev, code = x.shape[0], x.shape[1], x.device, _dtype_code(x)
-    _require(grad_y, "grad_y", x.dtype, dev)
-    _shape(grad_y, "grad_y", x.shape)
+    B, N, dev, code = x.shape[0], x.shape[1], x.device, _code(x)
+    _dense(grad_y, "grad_y", x.dtype, dev, x.shape)
     _given(state_in, "state_in", x.dtype, dev, (B, K - 1, D))
     _given(grad_state_out, "grad_state_out", x.dtype, dev, (B, K - 1, D))
     _lengths(lengths, dev, B)
-    with _on(dev, stream) as s:
+    on, s = _on(dev, stream)
+    with on:
         gx = torch.empty((B, N, D), dtype=x.dtype, device=dev)
         gw = torch.empty((D, K), dtype=weight.dtype, device=dev)
         gb = torch.empty(D, dtype=weight.dtype, device=dev) if bias is not None else None
@@ -379,10 +429,10 @@ def causal_conv_step(x, weight, state, bias=None, silu=False, out=None, stream=N
     up by one row in place."""
     torch = _torch()
     ldx, D, K, wcode = _conv_shapes(x, weight, bias, 2)
-    B, dev, code = x.shape[0], x.device, _dtype_code(x)
-    _require(state, "state", x.dtype, dev)
-    _shape(state, "state", (B, K - 1, D))
-    with _on(dev, stream) as s:
+    B, dev, code = x.shape[0], x.device, _code(x)
+    _dense(state, "state", x.dtype, dev, (B, K - 1, D))
+    on, s = _on(dev, stream)
+    with on:
         _given(out, "out", x.dtype, dev, (B, D))
         y = torch.empty((B, D), dtype=x.dtype, device=dev) if out is None else out
         _check(_fn("causal_conv_step")(_ptr(x), ldx, _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), B, D, K,
@@ -398,7 +448,7 @@ def _scan_shapes(x, dt, A, Bm, Cm, D, z, dt_bias, step):
     if x.dim() != (2 if step else 3):
         raise ValueError("x must be " + ("[B,D]" if step else "[B,N,D]"))
     dev, t, lead, ch = x.device, x.dtype, tuple(x.shape[:-1]), x.shape[-1]
-    code = _dtype_code(x)
+    code = _code(x)
     lddt = _rows(dt, "dt", t, dev, x.shape)
     ldz = _rows(z, "z", t, dev, x.shape) if z is not None else 0
     _require(A, "A", torch.float32, dev)
@@ -438,7 +488,8 @@ def selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=
     (B, N, ch), dev = x.shape, x.device
     _given(state_in, "state_in", torch.float32, dev, (B, ch, S))
     _lengths(lengths, dev, B)
-    with _on(dev, stream) as s:
+    on, s = _on(dev, stream)
+    with on:
         _given(out, "out", x.dtype, dev, (B, N, ch))
         _given(state_out, "state_out", torch.float32, dev, (B, ch, S))
         y = torch.empty((B, N, ch), dtype=x.dtype, device=dev) if out is None else out
@@ -460,12 +511,12 @@ def selective_scan_bwd(x, dt, A, Bm, Cm, grad_y, D=None, z=None, dt_bias=None, s
     torch = _torch()
     ld, G, S, code = _scan_shapes(x, dt, A, Bm, Cm, D, z, dt_bias, False)
     (B, N, ch), dev, t = x.shape, x.device, x.dtype
-    _require(grad_y, "grad_y", t, dev)
-    _shape(grad_y, "grad_y", x.shape)
+    _dense(grad_y, "grad_y", t, dev, x.shape)
     _given(state_in, "state_in", torch.float32, dev, (B, ch, S))
     _given(grad_state_out, "grad_state_out", torch.float32, dev, (B, ch, S))
     _lengths(lengths, dev, B)
-    with _on(dev, stream) as s:
+    on, s = _on(dev, stream)
+    with on:
         full = lambda: torch.empty((B, N, ch), dtype=t, device=dev)                         # noqa: E731
         f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)           # noqa: E731
         gx, gdt, gz = full(), full(), full() if z is not None else None
@@ -489,9 +540,9 @@ def selective_scan_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, s
     torch = _torch()
     ld, G, S, code = _scan_shapes(x, dt, A, Bm, Cm, D, z, dt_bias, True)
     (B, ch), dev = x.shape, x.device
-    _require(state, "state", torch.float32, dev)
-    _shape(state, "state", (B, ch, S))
-    with _on(dev, stream) as s:
+    _dense(state, "state", torch.float32, dev, (B, ch, S))
+    on, s = _on(dev, stream)
+    with on:
         _given(out, "out", x.dtype, dev, (B, ch))
         y = torch.empty((B, ch), dtype=x.dtype, device=dev) if out is None else out
         _check(_fn("selective_scan_step")(_ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
