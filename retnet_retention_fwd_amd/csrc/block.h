@@ -85,7 +85,7 @@ struct ConvArgs {
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_conv_step(const ConvArgs& a, hipStream_t stream);
-size_t conv_bwd_workspace(int B, int N, int D, int K, bool bf16);
+size_t conv_bwd_workspace(int B, int N, int D, int K);
 
 // Selective scan (scan.hip, scan_bwd.hip).
 struct ScanArgs {

@@ -320,7 +320,7 @@ retn_status causal_conv_fwd(const void* x, long long ldx, const void* weight, co
 
 size_t causal_conv_bwd_workspace_bytes(int B, int N, int D, int K, retn_dtype dtype) {
     if (!valid_dtype(dtype) || conv_sizes(B, N, D, K) != RETN_OK) return 0;
-    return retn::conv_bwd_workspace(B, N, D, K, dtype == RETN_BF16);
+    return retn::conv_bwd_workspace(B, N, D, K);
 }
 
 retn_status causal_conv_bwd(const void* x, long long ldx, const void* weight, const void* bias, const void* state_in,
@@ -333,7 +333,7 @@ retn_status causal_conv_bwd(const void* x, long long ldx, const void* weight, co
     if (ldx < D) return RETN_ERR_SHAPE;
     const size_t tokens = sz(B) * N, es = elem_bytes(dtype), we = elem_bytes(wdtype), sb = sz(B) * (K - 1) * D * es;
     // workgroups: a block of 32 channels or more of each sequence's tiles, whose sums the workspace holds
-    if (retn::conv_bwd_workspace(B, N, 1, 1, dtype == RETN_BF16) / 8 * (sz(D) / 32 + 1) >= kMaxGroups)
+    if (retn::conv_bwd_workspace(B, N, D, K) / (f32(D) * (K + 1)) * (sz(D) / 32 + 1) >= kMaxGroups)
         return RETN_ERR_UNSUPPORTED;
     if ((tokens > 0 && (x == nullptr || grad_y == nullptr || grad_x == nullptr)) || weight == nullptr) return RETN_ERR_NULL;
     const bool sums = grad_weight != nullptr || grad_bias != nullptr;
