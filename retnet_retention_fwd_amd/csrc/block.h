@@ -35,6 +35,7 @@ struct NormArgs {
     int D;
     float eps;
     bool bf16, w_bf16;
+    bool stream;               // set by the launchers: the output is too large for the caches
     float* workspace;
 };
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream);
@@ -80,6 +81,7 @@ struct ConvArgs {
     void* gb;                  // backward, may be null
     int B, N, D, K;
     bool silu, bf16, w_bf16;
+    bool stream;               // set by the launchers
     float* workspace;
 };
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream);
@@ -103,6 +105,7 @@ struct ScanArgs {
     float *gA, *gD, *gbias, *gstate_in;            // gD, gbias, gstate_in may be null
     int B, N, D, G, S;
     bool softplus, bf16;
+    bool stream;                                   // set by the launchers
     float* workspace;
 };
 struct ScanPlan {

@@ -53,8 +53,8 @@ __device__ __forceinline__ Raw<T, V> pack(const T* p, int left) {
     return raw_load_n<T, V>(p, WHOLE ? V : left);
 }
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void put(T* p, const float (&v)[V], int left) {
-    store_n<T, V>(p, v, WHOLE ? V : left);
+__device__ __forceinline__ void put(T* p, const float (&v)[V], int left, bool stream) {
+    store_n<T, V>(p, v, WHOLE ? V : left, stream);
 }
 
 // Row t of xs without the K-1 state rows counted: t < 0 is a state row.
@@ -118,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int pack
             }
 #pragma unroll
             for (int k = 0; k < kRows; ++k) {
-                if (t + k < end) put<T, WHOLE>(y, o[k], left);
+                if (t + k < end) put<T, WHOLE>(y, o[k], left, false);
                 y += a.D;
             }
 #pragma unroll
@@ -257,9 +257,10 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, int wide
                     for (int i = 0; i < V; ++i) gx_row[i] += up(r.v[i]);
                 }
                 if (i0 >= 0) {
-                    put<T, WHOLE>(gx + static_cast<size_t>(i0) * a.D, gx_row, left);
+                    put<T, WHOLE>(gx + static_cast<size_t>(i0) * a.D, gx_row, left, a.stream);
                 } else if (a.gstate_in != nullptr) {
-                    put<T, WHOLE>(static_cast<T*>(a.gstate_in) + (static_cast<size_t>(b) * (K - 1) + s) * a.D + c, gx_row, left);
+                    put<T, WHOLE>(static_cast<T*>(a.gstate_in) + (static_cast<size_t>(b) * (K - 1) + s) * a.D + c, gx_row, left,
+                                  false);
                 }
             }
         }
@@ -350,7 +351,9 @@ template <typename T, typename W>
 hipError_t go_typed(const ConvArgs& a, Way way, hipStream_t st) {
     return a.K == 2 ? go_k<T, W, 2>(a, way, st) : a.K == 3 ? go_k<T, W, 3>(a, way, st) : go_k<T, W, 4>(a, way, st);
 }
-hipError_t go(const ConvArgs& a, Way way, hipStream_t st) {
+hipError_t go(const ConvArgs& args, Way way, hipStream_t st) {
+    ConvArgs a = args;
+    a.stream = static_cast<size_t>(a.B) * a.N * a.D * (a.bf16 ? 2 : 4) >= kStreamBytes;
     if (!a.bf16) return go_typed<float, float>(a, way, st);
     return a.w_bf16 ? go_typed<bf16_t, bf16_t>(a, way, st) : go_typed<bf16_t, float>(a, way, st);
 }

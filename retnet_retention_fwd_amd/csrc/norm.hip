@@ -60,34 +60,56 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
         if (e < D && b != nullptr) br[p] = raw_load_n<W, V>(b + e, D - e);
     }
     const float inv = 1.f / static_cast<float>(D);
+    // the next row is in flight while one is worked on
+    Raw<T, V> next[P];
+    auto fetch = [&](size_t r) {
+        const T* xr = x + (r < a.rows ? r : a.rows - 1) * D;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * TPR + l) * V;
+            next[p] = Raw<T, V>{};
+            if (a.stream && e + V <= D)
+                next[p] = load_stream<T, V>(xr + e);
+            else if (e < D)
+                next[p] = raw_load_n<T, V>(xr + e, D - e);
+        }
+    };
+    const size_t stride = static_cast<size_t>(gridDim.x) * RPB;
+    fetch(static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / TPR);
     // a workgroup's rows share their trips, so the barriers of row_sum2 are uniform
-    for (size_t r0 = static_cast<size_t>(blockIdx.x) * RPB; r0 < a.rows; r0 += static_cast<size_t>(gridDim.x) * RPB) {
+    for (size_t r0 = static_cast<size_t>(blockIdx.x) * RPB; r0 < a.rows; r0 += stride) {
         const size_t r = r0 + threadIdx.x / TPR;
         const bool live = r < a.rows;
-        const T* xr = x + (live ? r : r0) * D;
         float v[P][V];
         float s = 0.f;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int e = (p * TPR + l) * V;
-            Raw<T, V> raw = {};
-            if (e < D) raw = raw_load_n<T, V>(xr + e, D - e);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                v[p][i] = up(raw.v[i]);
+                v[p][i] = up(next[p].v[i]);
                 s += v[p][i];
             }
         }
+        if (r0 + stride < a.rows) fetch(r + stride);
         float none = 0.f, q = 0.f;
         row_sum2<TPR>(s, none, red, slot);
         const float mean = s * inv;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int e = (p * TPR + l) * V;
+            // only the pack that the row ends in is masked element by element
+            if (e + V <= D) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                v[p][i] -= mean;
-                if (e + i < D) q = fmaf(v[p][i], v[p][i], q);
+                for (int i = 0; i < V; ++i) {
+                    v[p][i] -= mean;
+                    q = fmaf(v[p][i], v[p][i], q);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    v[p][i] -= mean;
+                    if (e + i < D) q = fmaf(v[p][i], v[p][i], q);
+                }
             }
         }
         none = 0.f;
@@ -109,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
                 if (w != nullptr) o[i] *= up(wr[p].v[i]);
                 if (b != nullptr) o[i] += up(br[p].v[i]);
             }
-            store_n<T, V>(y + r * D + e, o, D - e);
+            store_n<T, V>(y + r * D + e, o, D - e, a.stream);
         }
     }
 }
@@ -177,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
             float o[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) o[i] = rstd * (v[p][i] - fmaf(xh[p][i], m2, m1));
-            store_n<T, V>(gx + r * D + e, o, D - e);
+            store_n<T, V>(gx + r * D + e, o, D - e, a.stream);
         }
     }
     if (a.workspace == nullptr) return;
@@ -334,7 +356,7 @@ int bwd_blocks(size_t rows, int D) {
 template <typename T, typename W>
 hipError_t fwd_typed(const NormArgs& a, hipStream_t st) {
     const int D = a.D;
-    const bool wave = D <= kWaveF * 64;
+    const bool wave = D <= 1024;
     const size_t need = wave ? (a.rows + 3) / 4 : a.rows;
     const dim3 grid(static_cast<unsigned>(need < kMaxBlocks ? need : kMaxBlocks)), block(kThreads);
     ProfScope prof(kProfNorm, st);
@@ -342,8 +364,8 @@ hipError_t fwd_typed(const NormArgs& a, hipStream_t st) {
         hipLaunchKernelGGL((norm_fwd_kernel<T, W, 8, 64>), grid, block, 0, st, a);
     else if (D <= 1024)
         hipLaunchKernelGGL((norm_fwd_kernel<T, W, 16, 64>), grid, block, 0, st, a);
-    else if (wave)
-        hipLaunchKernelGGL((norm_fwd_kernel<T, W, 32, 64>), grid, block, 0, st, a);
+    else if (D <= 8 * kThreads)
+        hipLaunchKernelGGL((norm_fwd_kernel<T, W, 8, kThreads>), grid, block, 0, st, a);
     else if (D <= 16 * kThreads)
         hipLaunchKernelGGL((norm_fwd_kernel<T, W, 16, kThreads>), grid, block, 0, st, a);
     else if (D <= 32 * kThreads)
@@ -403,12 +425,16 @@ size_t norm_bwd_workspace(size_t rows, int D, bool) {
     return static_cast<size_t>(bwd_blocks(rows, D)) * 2 * D * sizeof(float);
 }
 
-hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t st) {
+hipError_t launch_norm_fwd(const NormArgs& args, hipStream_t st) {
+    NormArgs a = args;
+    a.stream = a.rows * a.D * (a.bf16 ? 2 : 4) >= kStreamBytes;
     if (!a.bf16) return fwd_typed<float, float>(a, st);
     return a.w_bf16 ? fwd_typed<bf16_t, bf16_t>(a, st) : fwd_typed<bf16_t, float>(a, st);
 }
 
-hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t st) {
+hipError_t launch_norm_bwd(const NormArgs& args, hipStream_t st) {
+    NormArgs a = args;
+    a.stream = a.rows * a.D * (a.bf16 ? 2 : 4) >= kStreamBytes;
     if (!a.bf16) return bwd_typed<float, float>(a, st);
     return a.w_bf16 ? bwd_typed<bf16_t, bf16_t>(a, st) : bwd_typed<bf16_t, float>(a, st);
 }

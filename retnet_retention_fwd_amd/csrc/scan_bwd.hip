@@ -346,8 +346,8 @@ __device__ __forceinline__ Raw<T, 4> pack_at(const T* base, uint32_t byte, int l
     return raw_load_n<T, 4>(reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + byte), WHOLE ? 4 : left);
 }
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void pack_put(T* base, uint32_t byte, const float (&v)[4], int left) {
-    store_n<T, 4>(reinterpret_cast<T*>(reinterpret_cast<char*>(base) + byte), v, WHOLE ? 4 : left);
+__device__ __forceinline__ void pack_put(T* base, uint32_t byte, const float (&v)[4], int left, bool stream = false) {
+    store_n<T, 4>(reinterpret_cast<T*>(reinterpret_cast<char*>(base) + byte), v, WHOLE ? 4 : left, stream);
 }
 
 // WHOLE: a group's channels and the states are multiples of 4, so that every pack is whole.
@@ -620,9 +620,9 @@ __global__ __launch_bounds__(kScanThreads, LPC == 16 ? 2 : 3) void scan_bwd_kern
             sgD[k2.id] = gD;
             sgbias[k2.id] = gbias;
             const size_t at = (tok0 + t0) * a.D;
-            pack_put<T, WHOLE>(gx + at, k2.off(a.D), ox, k2.left);
-            pack_put<T, WHOLE>(gdt + at, k2.off(a.D), odt, k2.left);
-            if (a.gz != nullptr) pack_put<T, WHOLE>(gz + at, k2.off(a.D), oz, k2.left);
+            pack_put<T, WHOLE>(gx + at, k2.off(a.D), ox, k2.left, a.stream);
+            pack_put<T, WHOLE>(gdt + at, k2.off(a.D), odt, k2.left, a.stream);
+            if (a.gz != nullptr) pack_put<T, WHOLE>(gz + at, k2.off(a.D), oz, k2.left, a.stream);
         }
     }
     // [B nseg][S + 2][D] partial sums of the parameters' gradients
@@ -745,7 +745,9 @@ ScanPlan scan_bwd_plan(int B, int N, int D, int G, int S) {
     return p;
 }
 
-hipError_t launch_scan_bwd(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
+hipError_t launch_scan_bwd(const ScanArgs& args, const ScanPlan& p, hipStream_t st) {
+    ScanArgs a = args;
+    a.stream = static_cast<size_t>(a.B) * a.N * a.D * (a.bf16 ? 2 : 4) >= kStreamBytes;
     return a.bf16 ? bwd_typed<bf16_t>(a, p, st) : bwd_typed<float>(a, p, st);
 }
 

@@ -17,9 +17,31 @@ template <typename T, int V>
 struct __attribute__((packed, aligned(sizeof(T)))) Raw {
     T v[V];
 };
+// They are moved as vectors of words, which the compiler keeps whole.  (As structures of
+// elements it splits them to share pieces with the element-wise loads of a cut pack.)
+template <int BYTES>
+struct Words {
+    typedef uint32_t type __attribute__((ext_vector_type(BYTES / 4)));
+};
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> raw_load(const T* p) {
-    return *reinterpret_cast<const Raw<T, V>*>(p);
+    if constexpr (sizeof(T) * V >= 4) {
+        typedef typename Words<sizeof(T) * V>::type W;
+        typedef W At __attribute__((aligned(sizeof(T))));
+        return __builtin_bit_cast(Raw<T, V>, static_cast<W>(*reinterpret_cast<const At*>(p)));
+    } else {
+        return *reinterpret_cast<const Raw<T, V>*>(p);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void raw_store(T* p, const Raw<T, V>& r) {
+    if constexpr (sizeof(T) * V >= 4) {
+        typedef typename Words<sizeof(T) * V>::type W;
+        typedef W At __attribute__((aligned(sizeof(T))));
+        *reinterpret_cast<At*>(p) = __builtin_bit_cast(W, r);
+    } else {
+        *reinterpret_cast<Raw<T, V>*>(p) = r;
+    }
 }
 template <typename T>
 __device__ __forceinline__ float up(T x) {
@@ -30,6 +52,27 @@ __device__ __forceinline__ T down(float x) {
     T r;
     io<T>::store(&r, x);
     return r;
+}
+// Loads and stores past the caches, for what is used once: large outputs (kStreamBytes) of the
+// normalisation and of the backward passes, which the caches would not hold until they are
+// read again.  Measured per kernel: normalisation of 16384 x 2048 bf16 38 us with plain
+// stores, 32 us with these, 30 us with loads too; convolution's gradient 33.6 and 32.2 us,
+// scan's 417 and 408 us; rotary positions got slower (51 and 56 us) and keep plain ones.
+constexpr size_t kStreamBytes = static_cast<size_t>(8) << 20;
+template <typename T, int V>
+__device__ __forceinline__ void store_stream(T* p, const Raw<T, V>& r) {
+    typedef typename Words<sizeof(T) * V>::type W;
+    typedef W At __attribute__((aligned(sizeof(T))));
+    asm volatile("");       // on both sides: else the compiler joins it with a plain store beside it
+    __builtin_nontemporal_store(__builtin_bit_cast(W, r), reinterpret_cast<At*>(p));
+    asm volatile("");
+}
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_stream(const T* p) {
+    typedef typename Words<sizeof(T) * V>::type W;
+    typedef W At __attribute__((aligned(sizeof(T))));
+    asm volatile("");
+    return __builtin_bit_cast(Raw<T, V>, static_cast<W>(__builtin_nontemporal_load(reinterpret_cast<const At*>(p))));
 }
 // The first `left` of V elements, zeros behind them (left >= V: one wide load).
 template <typename T, int V>
@@ -43,7 +86,7 @@ __device__ __forceinline__ Raw<T, V> raw_load_n(const T* p, int left) {
 template <typename T, int V>
 __device__ __forceinline__ void raw_store_n(T* p, const Raw<T, V>& r, int left) {
     if (left >= V) {
-        *reinterpret_cast<Raw<T, V>*>(p) = r;
+        raw_store<T, V>(p, r);
         return;
     }
 #pragma unroll
@@ -51,10 +94,16 @@ __device__ __forceinline__ void raw_store_n(T* p, const Raw<T, V>& r, int left) 
         if (i < left) p[i] = r.v[i];
 }
 template <typename T, int V>
-__device__ __forceinline__ void store_n(T* p, const float* x, int left) {
+__device__ __forceinline__ void store_n(T* p, const float* x, int left, bool stream = false) {
     Raw<T, V> r;
 #pragma unroll
     for (int i = 0; i < V; ++i) r.v[i] = down<T>(x[i]);
+    if constexpr (V * sizeof(T) >= 8) {
+        if (stream && left >= V) {
+            store_stream(p, r);
+            return;
+        }
+    }
     raw_store_n(p, r, left);
 }
 template <typename T>
