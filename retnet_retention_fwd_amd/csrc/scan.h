@@ -112,6 +112,12 @@ template <typename T>
 __device__ __forceinline__ T row_at(const T* row, uint32_t byte) {
     return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + byte);
 }
+// A stride whose multiples the compiler does not keep (eight of each tensor's would crowd the
+// scalar registers): rows are stepped through by adding it.
+__device__ __forceinline__ long long stepped(long long ld) {
+    asm volatile("" : "+s"(ld));
+    return ld;
+}
 template <typename T>
 __device__ __forceinline__ void row_put(T* row, uint32_t byte, T v) {
     *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + byte) = v;

@@ -66,21 +66,22 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
 
     T rx[kAhead], rdt[kAhead], rz[kAhead] = {};
     auto fetch = [&](int t0) {
-        const T* xr = xp + t0 * a.ldx;
-        const T* dr = dp + t0 * a.lddt;
-        const T* zr = zp + t0 * a.ldz;
+        const long long ldx = stepped(a.ldx), lddt = stepped(a.lddt), ldz = stepped(a.ldz);
+        const T* xr = xp + t0 * ldx;
+        const T* dr = dp + t0 * lddt;
+        const T* zr = zp + t0 * ldz;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             rx[k] = row_at(xr, at);
             rdt[k] = row_at(dr, at);
-            xr += a.ldx;
-            dr += a.lddt;
+            xr += ldx;
+            dr += lddt;
         }
         if (gated) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 rz[k] = row_at(zr, at);
-                zr += a.ldz;
+                zr += ldz;
             }
         }
     };
@@ -91,8 +92,9 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
         // between them are straight code
         float x[kAhead], dt[kAhead], z[kAhead], y[kAhead];
         WaveRow<T, SP, SCALAR> B[2], C[2];
-        const T* Bt = Bp + static_cast<size_t>(t) * a.ldb;
-        const T* Ct = Cp + static_cast<size_t>(t) * a.ldc;
+        const long long ldb = stepped(a.ldb), ldc = stepped(a.ldc);
+        const T* Bt = Bp + t * ldb;
+        const T* Ct = Cp + t * ldc;
         B[0].load(Bt, S);
         if (!STATE) C[0].load(Ct, S);
 #pragma unroll
@@ -110,8 +112,8 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
         for (int k = 0; k < kAhead; ++k) {
             rows_arrived<SCALAR>();
             if (k + 1 < kAhead) {
-                B[(k + 1) & 1].load(Bt += a.ldb, S);
-                if (!STATE) C[(k + 1) & 1].load(Ct += a.ldc, S);
+                B[(k + 1) & 1].load(Bt += ldb, S);
+                if (!STATE) C[(k + 1) & 1].load(Ct += ldc, S);
             }
             rows_issued<SCALAR>();
             y[k] = step(dt[k], x[k], B[k & 1], C[k & 1]);
@@ -122,11 +124,12 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
             for (int k = 0; k < kAhead; ++k) y[k] *= gate(z[k]);
         }
         if (on) {
-            T* yr = yp + static_cast<size_t>(t) * a.D;
+            const long long ldy = stepped(a.D);
+            T* yr = yp + t * ldy;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 row_put(yr, at, down<T>(y[k]));
-                yr += a.D;
+                yr += ldy;
             }
         }
     }

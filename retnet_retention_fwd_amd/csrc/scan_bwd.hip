@@ -73,14 +73,15 @@ __global__ __launch_bounds__(kScanThreads) void scan_keep_kernel(ScanArgs a, Sca
     };
     T rx[kAhead], rdt[kAhead];
     auto fetch = [&](int t0) {
-        const T* xr = xp + t0 * a.ldx;
-        const T* dr = dp + t0 * a.lddt;
+        const long long ldx = stepped(a.ldx), lddt = stepped(a.lddt);
+        const T* xr = xp + t0 * ldx;
+        const T* dr = dp + t0 * lddt;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             rx[k] = row_at(xr, lane_at);
             rdt[k] = row_at(dr, lane_at);
-            xr += a.ldx;
-            dr += a.lddt;
+            xr += ldx;
+            dr += lddt;
         }
     };
     int t = p.t_begin;
@@ -89,7 +90,8 @@ __global__ __launch_bounds__(kScanThreads) void scan_keep_kernel(ScanArgs a, Sca
         if (t % kTile == 0) keep(t);
         float x[kAhead], dt[kAhead];
         WaveRow<T, SP, SCALAR> B[2];
-        const T* Bt = Bp + static_cast<size_t>(t) * a.ldb;
+        const long long ldb = stepped(a.ldb);
+        const T* Bt = Bp + t * ldb;
         B[0].load(Bt, S);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
@@ -104,7 +106,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_keep_kernel(ScanArgs a, Sca
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             rows_arrived<SCALAR>();
-            if (k + 1 < kAhead) B[(k + 1) & 1].load(Bt += a.ldb, S);
+            if (k + 1 < kAhead) B[(k + 1) & 1].load(Bt += ldb, S);
             rows_issued<SCALAR>();
             step(dt[k], x[k], B[k & 1]);
         }
@@ -170,21 +172,22 @@ __global__ __launch_bounds__(kScanThreads) void scan_rev_kernel(ScanArgs a, Scan
     }
     T rdt[kAhead], rz[kAhead] = {}, rg[kAhead];
     auto fetch = [&](int t0) {
-        const T* dr = dp + t0 * a.lddt;
-        const T* gr = gp + static_cast<size_t>(t0) * a.D;
-        const T* zr = zp + t0 * a.ldz;
+        const long long lddt = stepped(a.lddt), ldg = stepped(a.D), ldz = stepped(a.ldz);
+        const T* dr = dp + t0 * lddt;
+        const T* gr = gp + t0 * ldg;
+        const T* zr = zp + t0 * ldz;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             rdt[k] = row_at(dr, lane_at);
             rg[k] = row_at(gr, lane_at);
-            dr += a.lddt;
-            gr += a.D;
+            dr += lddt;
+            gr += ldg;
         }
         if (gated) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 rz[k] = row_at(zr, lane_at);
-                zr += a.ldz;
+                zr += ldz;
             }
         }
     };
@@ -193,7 +196,8 @@ __global__ __launch_bounds__(kScanThreads) void scan_rev_kernel(ScanArgs a, Scan
         const int t = p.t_begin + blk * kAhead;
         float dt[kAhead], g[kAhead], z[kAhead];
         WaveRow<T, SP, SCALAR> C[2];
-        const T* Ct = Cp + static_cast<size_t>(t + kAhead - 1) * a.ldc;
+        const long long ldc = stepped(a.ldc);
+        const T* Ct = Cp + (t + kAhead - 1) * ldc;
         C[(kAhead - 1) & 1].load(Ct, S);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
@@ -213,7 +217,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_rev_kernel(ScanArgs a, Scan
 #pragma unroll
         for (int k = kAhead - 1; k >= 0; --k) {
             rows_arrived<SCALAR>();
-            if (k > 0) C[(k - 1) & 1].load(Ct -= a.ldc, S);
+            if (k > 0) C[(k - 1) & 1].load(Ct -= ldc, S);
             rows_issued<SCALAR>();
             step(dt[k], g[k], C[k & 1]);
         }

@@ -113,14 +113,13 @@ __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x);
 // 1 / (1 + e^-x).  The exponent's rounding is relative to x (|x| 2^-24 of e^-x), which the
 // bounded x of a gate keeps near the rounding of its own type.
 __device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + __builtin_amdgcn_exp2f(x * -kLog2e)); }
-// log(1 + e^x), x itself above 20 (the difference there is below half a unit of x).  The
-// logarithm of w = 1 + e is divided by (w - 1) / e, which takes out the rounding of w: small
-// e would lose all of its digits there.
+// log(1 + e^x).  With w = 1 + e rounded, the logarithm of w lacks log(1 + c / w), c = e - (w - 1)
+// being what the rounding lost (all of e, where e is small).  Where e^x overflows the sum is
+// no number and the maximum takes x, which softplus then is; a NaN stays one.
 __device__ __forceinline__ float softplus_f(float x) {
-    const float e = __builtin_amdgcn_exp2f((x > 20.f ? 20.f : x) * kLog2e);
-    const float w = 1.f + e, d = w - 1.f;
-    const float l = d > 0.f ? __builtin_amdgcn_logf(w) * 0.693147180559945f * (e * rcp(d)) : e;
-    return x <= 20.f ? l : x;
+    const float e = __builtin_amdgcn_exp2f(x * kLog2e);
+    const float w = 1.f + e, c = e - (w - 1.f);
+    return fmaxf(fmaf(c, rcp(w), __builtin_amdgcn_logf(w) * 0.693147180559945f), x);
 }
 
 // Exchange with the lane whose number differs in the bits of MASK, for the masks that one
