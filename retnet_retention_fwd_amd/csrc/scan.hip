@@ -67,20 +67,21 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
     T rx[kAhead], rdt[kAhead], rz[kAhead] = {};
     auto fetch = [&](int t0) {
         const long long ldx = stepped(a.ldx), lddt = stepped(a.lddt), ldz = stepped(a.ldz);
+        const uint32_t lane = opaque(at);      // added last, by the load itself
         const T* xr = xp + t0 * ldx;
         const T* dr = dp + t0 * lddt;
         const T* zr = zp + t0 * ldz;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            rx[k] = row_at(xr, at);
-            rdt[k] = row_at(dr, at);
+            rx[k] = row_at(xr, lane);
+            rdt[k] = row_at(dr, lane);
             xr += ldx;
             dr += lddt;
         }
         if (gated) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                rz[k] = row_at(zr, at);
+                rz[k] = row_at(zr, lane);
                 zr += ldz;
             }
         }
@@ -125,10 +126,11 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
         }
         if (on) {
             const long long ldy = stepped(a.D);
+            const uint32_t lane = opaque(at);
             T* yr = yp + t * ldy;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                row_put(yr, at, down<T>(y[k]));
+                row_put(yr, lane, down<T>(y[k]));
                 yr += ldy;
             }
         }

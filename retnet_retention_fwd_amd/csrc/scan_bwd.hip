@@ -74,12 +74,13 @@ __global__ __launch_bounds__(kScanThreads) void scan_keep_kernel(ScanArgs a, Sca
     T rx[kAhead], rdt[kAhead];
     auto fetch = [&](int t0) {
         const long long ldx = stepped(a.ldx), lddt = stepped(a.lddt);
+        const uint32_t at = opaque(lane_at);   // added last, by the load itself
         const T* xr = xp + t0 * ldx;
         const T* dr = dp + t0 * lddt;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            rx[k] = row_at(xr, lane_at);
-            rdt[k] = row_at(dr, lane_at);
+            rx[k] = row_at(xr, at);
+            rdt[k] = row_at(dr, at);
             xr += ldx;
             dr += lddt;
         }
@@ -173,20 +174,21 @@ __global__ __launch_bounds__(kScanThreads) void scan_rev_kernel(ScanArgs a, Scan
     T rdt[kAhead], rz[kAhead] = {}, rg[kAhead];
     auto fetch = [&](int t0) {
         const long long lddt = stepped(a.lddt), ldg = stepped(a.D), ldz = stepped(a.ldz);
+        const uint32_t at = opaque(lane_at);
         const T* dr = dp + t0 * lddt;
         const T* gr = gp + t0 * ldg;
         const T* zr = zp + t0 * ldz;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            rdt[k] = row_at(dr, lane_at);
-            rg[k] = row_at(gr, lane_at);
+            rdt[k] = row_at(dr, at);
+            rg[k] = row_at(gr, at);
             dr += lddt;
             gr += ldg;
         }
         if (gated) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                rz[k] = row_at(zr, lane_at);
+                rz[k] = row_at(zr, at);
                 zr += ldz;
             }
         }
