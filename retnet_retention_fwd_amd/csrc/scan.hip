@@ -163,7 +163,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_compose_kernel(ScanArgs a, 
     float* end = a.workspace + pl.off_end + b * pl.nseg * ds + e;
     const float* sum = a.workspace + pl.off_dt + b * pl.nseg * a.D + e / a.S;
     float h = a.state_in != nullptr ? a.state_in[id] : 0.f;
-    constexpr int U = 4;           // segments whose loads are in flight together
+    constexpr int U = 16;          // segments whose loads are in flight together
     for (int s0 = 0; s0 < pl.nseg - 1; s0 += U) {
         float own[U], dt[U];
 #pragma unroll

@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_compose_both_kernel(ScanArg
     float* end = a.workspace + pl.off_end + b * pl.nseg * ds + e;
     float* rev = a.workspace + pl.off_rev + b * pl.nseg * ds + e;
     const float* sum = a.workspace + pl.off_dt + b * pl.nseg * a.D + e / a.S;
-    constexpr int U = 4;           // segments whose loads are in flight together
+    constexpr int U = 8;           // segments whose loads are in flight together
     float own[U], dec[U];
     float h = a.state_in != nullptr ? a.state_in[id] : 0.f;
     for (int s0 = 0; s0 < pl.nseg; s0 += U) {
