@@ -339,8 +339,9 @@ double retention_calib_mfma_flops(int blocks, int waves, int iters);
  *              lengths[b] tokens (clamped to 0 .. N); what lies behind them is not read,
  *              output rows there are left as they were, gradient rows there are zero, and
  *              a final state is the one behind the last of those tokens.
- *   Limits     D <= 2^20, B * N < 2^31, B * D < 2^31, B * N * D < 2^34 (rotary: B * N * d
- *              < 2^32); else RETN_ERR_UNSUPPORTED.
+ *   Limits     D <= 2^20, B * N <= 2^31 - 2^16, B * D < 2^31, B * N * D < 2^34 (rotary:
+ *              B * N * d < 2^32, Hq + Hk < 2^16), row strides < 2^26; else
+ *              RETN_ERR_UNSUPPORTED.
  * All results are the same from call to call (no atomics).
  */
 

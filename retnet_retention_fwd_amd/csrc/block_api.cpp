@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <utility>
 
 #include "block.h"
@@ -20,6 +21,9 @@ constexpr int kMaxStates = 64;
 constexpr int kMaxHead = 256;
 constexpr unsigned long long kMaxElements = 1ull << 34;   // of a [B, N, D] tensor
 constexpr unsigned long long kMaxGroups = 1ull << 23;     // workgroups of a launch (2^32 threads at most)
+constexpr long long kMaxRow = 1ll << 26;                  // elements from one token to the next
+constexpr long long kMaxSpan = 1ll << 40;                 // elements that one axis of a view spans
+constexpr size_t kMaxTokens = (1ull << 31) - (1 << 16);   // token numbers and steps ahead of them are ints
 
 size_t sz(long long x) { return static_cast<size_t>(x); }
 size_t f32(size_t n) { return n * sizeof(float); }
@@ -61,7 +65,7 @@ retn_status norm_sizes(long long rows, int D) {
 // Sizes of a [B, N, D] operator.
 retn_status seq_sizes(int B, int N, int D) {
     if (B < 0 || N < 0 || D < 1) return RETN_ERR_SHAPE;
-    if (D > kMaxD || sz(B) * N > sz(INT32_MAX) || sz(B) * D > sz(INT32_MAX) || sz(B) * N * D >= kMaxElements)
+    if (D > kMaxD || sz(B) * N > kMaxTokens || sz(B) * D > sz(INT32_MAX) || sz(B) * N * D >= kMaxElements)
         return RETN_ERR_UNSUPPORTED;
     return RETN_OK;
 }
@@ -84,6 +88,10 @@ retn_status scan_sizes(int B, int N, int D, int G, int S) {
     return RETN_OK;
 }
 
+bool far_rows(long long ldx, long long lddt, long long ldz, long long ldb, long long ldc) {
+    return std::max({ldx, lddt, ldz, ldb, ldc}) >= kMaxRow;
+}
+
 bool bad_workspace(const void* p, size_t have, size_t need) {
     return need > 0 && (p == nullptr || have < need || !aligned16(p));
 }
@@ -97,7 +105,11 @@ size_t view_bytes(const View& v, int B, int H, int N, int d, size_t es) {
     return ((sz(B) - 1) * sz(v.sb) + (sz(H) - 1) * sz(v.sh) + (sz(N) - 1) * sz(v.sn) + d) * es;
 }
 bool valid_view(const View& v, int B, int H, int N) {
-    return (B <= 1 || v.sb >= 0) && (H <= 1 || v.sh >= 0) && (N <= 1 || v.sn >= 0);
+    const long long st[3] = {v.sb, v.sh, v.sn};
+    const int n[3] = {B, H, N};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (st[i] < 0 || st[i] > kMaxSpan / n[i])) return false;
+    return true;
 }
 // Every element of an output has a place of its own: sorted by stride, each axis steps
 // over all that the smaller ones span.
@@ -140,7 +152,8 @@ retn_status rotary_common(const void* q, const void* k, void* out_q, void* out_k
     if (!valid_dtype(dtype)) return RETN_ERR_DTYPE;
     if (B < 0 || Hq < 0 || Hk < 0 || N < 0 || d < 1 || rot < 2 || rot > d || rot % 2 != 0 || table_len < 0)
         return RETN_ERR_SHAPE;
-    if (d > kMaxHead || sz(B) * N > sz(INT32_MAX) || sz(B) * N * d >= (1ull << 32) || Hq > 65535 || Hk > 65535)
+    if (d > kMaxHead || sz(B) * N > kMaxTokens || sz(B) * N * d >= (1ull << 32) || sz(Hq) + Hk > 65535 ||
+        table_len > kMaxSpan)
         return RETN_ERR_UNSUPPORTED;
     if (B == 0 || N == 0 || Hq + Hk == 0) return RETN_OK;
     if ((Hq > 0 && (q == nullptr || out_q == nullptr)) || (Hk > 0 && (k == nullptr || out_k == nullptr)) ||
@@ -291,6 +304,7 @@ retn_status causal_conv_fwd(const void* x, long long ldx, const void* weight, co
     const retn_status st = conv_sizes(B, N, D, K);
     if (st != RETN_OK) return st;
     if (ldx < D) return RETN_ERR_SHAPE;
+    if (ldx >= kMaxRow) return RETN_ERR_UNSUPPORTED;
     const size_t tokens = sz(B) * N, es = elem_bytes(dtype), we = elem_bytes(wdtype), sb = sz(B) * (K - 1) * D * es;
     if (B == 0) return RETN_OK;
     if ((N > 0 && (x == nullptr || y == nullptr)) || weight == nullptr) return RETN_ERR_NULL;
@@ -331,6 +345,7 @@ retn_status causal_conv_bwd(const void* x, long long ldx, const void* weight, co
     const retn_status st = conv_sizes(B, N, D, K);
     if (st != RETN_OK) return st;
     if (ldx < D) return RETN_ERR_SHAPE;
+    if (ldx >= kMaxRow) return RETN_ERR_UNSUPPORTED;
     const size_t tokens = sz(B) * N, es = elem_bytes(dtype), we = elem_bytes(wdtype), sb = sz(B) * (K - 1) * D * es;
     // workgroups: a block of 32 channels or more of each sequence's tiles, whose sums the workspace holds
     if (retn::conv_bwd_workspace(B, N, D, K) / (f32(D) * (K + 1)) * (sz(D) / 32 + 1) >= kMaxGroups)
@@ -376,6 +391,7 @@ retn_status causal_conv_step(const void* x, long long ldx, const void* weight, c
     const retn_status st = conv_sizes(B, 1, D, K);
     if (st != RETN_OK) return st;
     if (ldx < D) return RETN_ERR_SHAPE;
+    if (ldx >= kMaxRow) return RETN_ERR_UNSUPPORTED;
     if (B == 0) return RETN_OK;
     if (x == nullptr || weight == nullptr || state == nullptr || y == nullptr) return RETN_ERR_NULL;
     const size_t es = elem_bytes(dtype), we = elem_bytes(wdtype);
@@ -414,6 +430,7 @@ retn_status selective_scan_fwd(const void* x, const void* dt, const float* A, co
     if (st != RETN_OK) return st;
     const long long gs = static_cast<long long>(G) * S;
     if (ldx < D || lddt < D || (z != nullptr && ldz < D) || ldb < gs || ldc < gs) return RETN_ERR_SHAPE;
+    if (far_rows(ldx, lddt, z != nullptr ? ldz : 0, ldb, ldc)) return RETN_ERR_UNSUPPORTED;
     if (B == 0) return RETN_OK;
     const size_t tokens = sz(B) * N, es = elem_bytes(dtype), ss = f32(sz(B) * D * S);
     if (N > 0 && (x == nullptr || dt == nullptr || A == nullptr || Bm == nullptr || Cm == nullptr || y == nullptr))
@@ -476,6 +493,7 @@ retn_status selective_scan_bwd(const void* x, const void* dt, const float* A, co
     if (st != RETN_OK) return st;
     const long long gs = static_cast<long long>(G) * S;
     if (ldx < D || lddt < D || (z != nullptr && ldz < D) || ldb < gs || ldc < gs) return RETN_ERR_SHAPE;
+    if (far_rows(ldx, lddt, z != nullptr ? ldz : 0, ldb, ldc)) return RETN_ERR_UNSUPPORTED;
     const size_t tokens = sz(B) * N, es = elem_bytes(dtype), ss = f32(sz(B) * D * S);
     if (tokens > 0 && (x == nullptr || dt == nullptr || A == nullptr || Bm == nullptr || Cm == nullptr || grad_y == nullptr ||
                        grad_x == nullptr || grad_dt == nullptr || grad_B == nullptr || grad_C == nullptr ||
@@ -542,6 +560,7 @@ retn_status selective_scan_step(const void* x, const void* dt, const float* A, c
     if (st != RETN_OK) return st;
     const long long gs = static_cast<long long>(G) * S;
     if (ldx < D || lddt < D || (z != nullptr && ldz < D) || ldb < gs || ldc < gs) return RETN_ERR_SHAPE;
+    if (far_rows(ldx, lddt, z != nullptr ? ldz : 0, ldb, ldc)) return RETN_ERR_UNSUPPORTED;
     if (B == 0) return RETN_OK;
     if (x == nullptr || dt == nullptr || A == nullptr || Bm == nullptr || Cm == nullptr || state == nullptr || y == nullptr)
         return RETN_ERR_NULL;

@@ -76,6 +76,8 @@ def test_rotary(name):
     assert c(first=-1) == ERR_SHAPE and c(first=93) == ERR_SHAPE and c(length=7) == ERR_SHAPE and c(length=-1) == ERR_SHAPE
     assert c(d=258, rot=64) == ERR_UNSUPPORTED and c(B=1 << 20, N=1 << 10) == ERR_UNSUPPORTED
     assert c(B=1 << 16, N=1 << 20) == ERR_UNSUPPORTED
+    assert c(Hq=40000, Hk=40000) == ERR_UNSUPPORTED and c(length=1 << 62) == ERR_UNSUPPORTED
+    assert c(st=strides(q=(1 << 62, 512, 64))) == ERR_SHAPE and c(st=strides(oq=(2048, 1 << 62, 64))) == ERR_SHAPE
     assert c(q=None) == ERR_NULL and c(ok=None) == ERR_NULL and c(table=None) == ERR_NULL and c(st=None) == ERR_NULL
     assert c(st=strides(q=(-1, 512, 64))) == ERR_SHAPE
     assert c(oq=at(0) + 128) == ERR_ALIAS                       # partly over its input
@@ -115,6 +117,7 @@ def test_causal_conv(f):
     assert f(B=-1) == ERR_SHAPE and f(D=0) == ERR_SHAPE and f(K=0) == ERR_SHAPE and f(ldx=63) == ERR_SHAPE
     assert f(K=1) == ERR_UNSUPPORTED and f(K=5) == ERR_UNSUPPORTED
     assert f(B=1 << 20, D=1 << 14, ldx=1 << 14) == ERR_UNSUPPORTED
+    assert f(ldx=1 << 26) == ERR_UNSUPPORTED and f(ldx=1 << 62) == ERR_UNSUPPORTED
     assert f(x=None) == ERR_NULL and f(w=None) == ERR_NULL
 
 
@@ -130,6 +133,7 @@ def test_causal_conv_buffers():
     assert need > 0 and conv_bwd(ws=None) == ERR_WORKSPACE and conv_bwd(wsb=need - 1) == ERR_WORKSPACE
     assert conv_bwd(ws=at(11) + 8) == ERR_WORKSPACE
     assert conv_bwd(B=1 << 26, N=1, D=1, ldx=1) == ERR_UNSUPPORTED       # more workgroups than a launch takes
+    assert conv_bwd(B=1, N=(1 << 31) - 1, D=1, ldx=1) == ERR_UNSUPPORTED   # steps ahead of a token would wrap
     assert conv_bwd(N=0, gw=None, gb=None, gsi=None, ws=None) == OK
 
 
@@ -160,7 +164,8 @@ def test_selective_scan(f):
     assert f(G=3, ldb=48, ldc=48) == ERR_SHAPE                  # groups that do not divide the channels
     for ld in ("ldx", "lddt", "ldz"):
         assert f(**{ld: 63}) == ERR_SHAPE
-    assert f(ldb=15) == ERR_SHAPE and f(ldc=15) == ERR_SHAPE
+        assert f(**{ld: 1 << 26}) == ERR_UNSUPPORTED
+    assert f(ldb=15) == ERR_SHAPE and f(ldc=15) == ERR_SHAPE and f(ldb=1 << 62) == ERR_UNSUPPORTED
     assert f(S=65, ldb=65, ldc=65) == ERR_UNSUPPORTED
     assert f(B=1 << 20, ch=1 << 12, ldx=1 << 12, lddt=1 << 12, ldz=1 << 12) == ERR_UNSUPPORTED
     for p in ("x", "dt", "A", "Bm", "Cm"):

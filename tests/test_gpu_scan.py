@@ -80,7 +80,7 @@ CASES = [
     (1, 1, 1, 1, 1, False), (2, 3, 5, 1, 16, False), (1, 33, 64, 1, 16, True), (2, 70, 100, 2, 16, False),
     (1, 64, 96, 3, 8, True), (2, 40, 48, 1, 32, False), (1, 50, 40, 2, 20, True), (1, 45, 24, 1, 64, False),
     (1, 37, 17, 1, 47, True), (1, 600, 66, 1, 16, False), (1, 300, 20, 1, 33, False), (1, 520, 12, 4, 4, True),
-    (3, 129, 130, 1, 13, False),
+    (3, 129, 130, 1, 13, False), (2, 40, 128, 1, 8, False), (1, 90, 36, 1, 8, True), (40, 33, 260, 2, 16, False),
 ]
 
 
