@@ -6,7 +6,7 @@
 //     dw = sum over rows of gy xh,    db = sum over rows of gy
 //
 // Bound by HBM: forward reads and writes a row once, backward reads two and writes one.  A
-// row stays in the registers of one wave (up to 2048 columns) or of one workgroup, so the
+// row stays in the registers of one wave (up to 1024 columns) or of one workgroup, so the
 // mean is known before the squared deviations are summed: no cancellation, one read.  The
 // waves walk over rows with the weights in registers; in the backward each keeps its
 // columns' sums of gy xh and gy over all of its rows, the workgroup adds its waves' sums
@@ -22,23 +22,31 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sums of two values over the TPR threads that share a row.
+// Threads of a workgroup whose rows take TPR threads each.
+constexpr int threads_of(int tpr) { return tpr > kThreads ? tpr : kThreads; }
+
+// Sums of two values over the TPR threads that share a row (red: 4 TPR / 64 floats).
 template <int TPR>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float* red, int& slot) {
     a = wave_sum(a);
     b = wave_sum(b);
     if (TPR > 64) {
         // two sets of slots in turn: the next call writes one that nobody still reads
-        float* r = red + slot * 8;
+        constexpr int WV = TPR / 64;
+        float* r = red + slot * 2 * WV;
         slot ^= 1;
         const int wave = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) {
             r[wave] = a;
-            r[4 + wave] = b;
+            r[WV + wave] = b;
         }
         __syncthreads();
-        a = r[0] + r[1] + r[2] + r[3];
-        b = r[4] + r[5] + r[6] + r[7];
+        a = b = 0.f;
+#pragma unroll
+        for (int i = 0; i < WV; ++i) {
+            a += r[i];
+            b += r[WV + i];
+        }
     }
 }
 
@@ -137,9 +145,9 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a) {
 }
 
 template <typename T, typename W, int F, int TPR>
-__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
-    constexpr int V = kPack<T>, P = F / V, RPB = kThreads / TPR;
-    __shared__ float red[16];
+__global__ __launch_bounds__(threads_of(TPR)) void norm_bwd_kernel(NormArgs a) {
+    constexpr int V = kPack<T>, P = F / V, RPB = threads_of(TPR) / TPR;
+    __shared__ float red[TPR / 16];
     __shared__ float col[RPB > 1 ? RPB * F * 64 : 1];
     int slot = 0;
     const int l = threadIdx.x % TPR, D = a.D;
@@ -152,27 +160,39 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int e = (p * TPR + l) * V;
+        wr[p] = Raw<W, V>{};       // zeros behind the last column, where the gradient is zero too
         if (e < D && w != nullptr) wr[p] = raw_load_n<W, V>(w + e, D - e);
 #pragma unroll
         for (int i = 0; i < V; ++i) gw[p][i] = gb[p][i] = 0.f;
     }
     const float inv = 1.f / static_cast<float>(D);
-    for (size_t r0 = static_cast<size_t>(blockIdx.x) * RPB; r0 < a.rows; r0 += static_cast<size_t>(gridDim.x) * RPB) {
-        const size_t r = r0 + threadIdx.x / TPR;
-        const bool live = r < a.rows;
-        const T* xr = x + (live ? r : r0) * D;
-        const T* gr = gy + (live ? r : r0) * D;
-        Raw<T, V> rx[P], rg[P];
+    // the next row is in flight while one is worked on, where registers allow it
+    constexpr bool AHEAD = F <= 16;
+    Raw<T, V> rx[P], rg[P];
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&](size_t r) {
+        const bool there = r < a.rows;
+        const T* xr = x + (there ? r : 0) * D;
+        const T* gr = gy + (there ? r : 0) * D;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int e = (p * TPR + l) * V;
             rx[p] = rg[p] = Raw<T, V>{};
-            if (live && e < D) {
+            if (there && e < D) {
                 rx[p] = raw_load_n<T, V>(xr + e, D - e);
                 rg[p] = raw_load_n<T, V>(gr + e, D - e);
             }
         }
-        const float mean = live ? a.mean[r] : 0.f, rstd = live ? a.rstd[r] : 0.f;
+        mean = there ? a.mean[r] : 0.f;
+        rstd = there ? a.rstd[r] : 0.f;
+    };
+    const size_t stride = static_cast<size_t>(gridDim.x) * RPB;
+    if (AHEAD) fetch(static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / TPR);
+    for (size_t r0 = static_cast<size_t>(blockIdx.x) * RPB; r0 < a.rows; r0 += stride) {
+        const size_t r = r0 + threadIdx.x / TPR;
+        const bool live = r < a.rows;
+        if (!AHEAD) fetch(r);
+        const float scale = rstd;
         float xh[P][V], v[P][V], s = 0.f, sx = 0.f;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
@@ -183,12 +203,11 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
                 gw[p][i] = fmaf(g, xh[p][i], gw[p][i]);
                 gb[p][i] += g;
                 v[p][i] = w != nullptr ? g * up(wr[p].v[i]) : g;
-                if (((p * TPR + l) * V) + i < D) {
-                    s += v[p][i];
-                    sx = fmaf(v[p][i], xh[p][i], sx);
-                }
+                s += v[p][i];
+                sx = fmaf(v[p][i], xh[p][i], sx);
             }
         }
+        if (AHEAD && r0 + stride < a.rows) fetch(r + stride);
         row_sum2<TPR>(s, sx, red, slot);
         if (!live) continue;
         const float m1 = s * inv, m2 = sx * inv;
@@ -198,7 +217,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a) {
             if (e >= D) continue;
             float o[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = rstd * (v[p][i] - fmaf(xh[p][i], m2, m1));
+            for (int i = 0; i < V; ++i) o[i] = scale * (v[p][i] - fmaf(xh[p][i], m2, m1));
             store_n<T, V>(gx + r * D + e, o, D - e, a.stream);
         }
     }
@@ -341,16 +360,18 @@ __global__ __launch_bounds__(kRedCols* kRedGroups) void col_reduce_kernel(ColRed
     }
 }
 
-constexpr int kWaveF = 32, kGroupF = 64, kGroupBwdF = 32;   // floats of a row per lane
+constexpr int kGroupF = 64;                                 // floats of a row per thread, forward
 constexpr int kMaxBlocks = 2048;                            // forward workgroups: 8 per CU
-constexpr int kBwdBlocks = 512;                             // each leaves 2 D partial sums
+constexpr int kWideBwd = 16 * 1024;                         // columns above which rows are read again
 constexpr int kWideChunks = 64;
 
+// Workgroups of the backward: each leaves 2 D partial sums, so few; enough to fill the chip
+// (for 16384 rows of 2048: 61 us with 512 of them, 55 us with 768 or 1024).
 int bwd_blocks(size_t rows, int D) {
-    if (D > kGroupBwdF * kThreads) return kWideChunks;
-    const size_t rpb = D <= kWaveF * 64 ? 4 : 1;
+    if (D > kWideBwd) return kWideChunks;
+    const size_t rpb = D <= 1024 ? 4 : 1, most = D <= 1024 ? 512 : D <= 2048 ? 768 : D <= 4096 ? 512 : 256;
     const size_t n = (rows + rpb - 1) / rpb;
-    return static_cast<int>(n < kBwdBlocks ? n : kBwdBlocks);
+    return static_cast<int>(n < most ? n : most);
 }
 
 template <typename T, typename W>
@@ -387,12 +408,14 @@ hipError_t bwd_typed(const NormArgs& a, hipStream_t st) {
             hipLaunchKernelGGL((norm_bwd_kernel<T, W, 8, 64>), grid, block, 0, st, a);
         else if (D <= 1024)
             hipLaunchKernelGGL((norm_bwd_kernel<T, W, 16, 64>), grid, block, 0, st, a);
-        else if (D <= kWaveF * 64)
-            hipLaunchKernelGGL((norm_bwd_kernel<T, W, 32, 64>), grid, block, 0, st, a);
-        else if (D <= 16 * kThreads)
-            hipLaunchKernelGGL((norm_bwd_kernel<T, W, 16, kThreads>), grid, block, 0, st, a);
-        else if (D <= kGroupBwdF * kThreads)
-            hipLaunchKernelGGL((norm_bwd_kernel<T, W, kGroupBwdF, kThreads>), grid, block, 0, st, a);
+        else if (D <= 2048)
+            hipLaunchKernelGGL((norm_bwd_kernel<T, W, 8, 256>), grid, block, 0, st, a);
+        else if (D <= 4096)
+            hipLaunchKernelGGL((norm_bwd_kernel<T, W, 8, 512>), grid, dim3(512), 0, st, a);
+        else if (D <= 8192)
+            hipLaunchKernelGGL((norm_bwd_kernel<T, W, 8, 1024>), grid, dim3(1024), 0, st, a);
+        else if (D <= kWideBwd)
+            hipLaunchKernelGGL((norm_bwd_kernel<T, W, 16, 1024>), grid, dim3(1024), 0, st, a);
         else {
             const dim3 rows(static_cast<unsigned>(a.rows < kMaxBlocks ? a.rows : kMaxBlocks));
             hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>), rows, block, 0, st, a);
