@@ -176,7 +176,7 @@ def selective_scan_bwd(x, dt, A, Bm, Cm, grad_y, D=None, z=None, dt_bias=None, u
                 zt = _f64(z)[b, t]
                 s = _sigmoid(zt)
                 ys = np.sum(Cm[b, t][group] * hs[t + 1], -1) + skip * x[b, t]
-                gz[b, t] = gt * ys * a(s + zt * s * (1 - s))
+                gz[b, t] = gt * ys * (a(s) + a(zt * s * (1 - s)))
                 gt = gt * a(zt * s)
             adj = Cm[b, t][group] * gt[:, None] + w[b]
             dec = np.exp(dt[b, t][:, None] * A)

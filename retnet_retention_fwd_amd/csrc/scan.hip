@@ -154,32 +154,19 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
     }
 }
 
-// Entry states of a sequence's segments in place of their predecessors' end states.
-__global__ __launch_bounds__(kScanThreads) void scan_compose_kernel(ScanArgs a, ScanPlan pl) {
-    const size_t ds = static_cast<size_t>(a.D) * a.S, id = static_cast<size_t>(blockIdx.x) * kScanThreads + threadIdx.x;
-    if (id >= ds * a.B) return;
-    const size_t b = id / ds, e = id % ds;
-    const float A2 = a.A[e] * kLog2e;
-    float* end = a.workspace + pl.off_end + b * pl.nseg * ds + e;
-    const float* sum = a.workspace + pl.off_dt + b * pl.nseg * a.D + e / a.S;
-    float h = a.state_in != nullptr ? a.state_in[id] : 0.f;
-    constexpr int U = 16;          // segments whose loads are in flight together
-    for (int s0 = 0; s0 < pl.nseg - 1; s0 += U) {
-        float own[U], dt[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const bool in = s0 + k < pl.nseg - 1;
-            own[k] = in ? end[(s0 + k) * ds] : 0.f;
-            dt[k] = in ? sum[static_cast<size_t>(s0 + k) * a.D] : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (s0 + k >= pl.nseg - 1) break;
-            end[(s0 + k) * ds] = h;
-            h = fmaf(exp2_fast(A2 * dt[k]), h, own[k]);
-        }
-    }
-    end[(pl.nseg - 1) * ds] = h;
+// Entry states of the segments in place of their end states.
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void scan_compose_kernel(ScanArgs a, ScanPlan pl) {
+    __shared__ ComposeSums<WAVES> sums;
+    const size_t ds = static_cast<size_t>(a.D) * a.S, id = static_cast<size_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
+    // The last workgroup's idle lanes walk no segment: the walk is in place, and a pair has one owner.
+    const bool live = id < ds * a.B;
+    const size_t in = live ? id : 0;
+    const int nseg = live ? pl.nseg : 0;
+    const size_t b = in / ds, e = in % ds;
+    compose<WAVES, false>(a.workspace + pl.off_end + b * pl.nseg * ds + e,
+                          a.workspace + pl.off_dt + b * pl.nseg * a.D + e / a.S, ds, a.D, nseg, a.A[e] * kLog2e,
+                          a.state_in != nullptr ? a.state_in[in] : 0.f, sums);
 }
 
 // One token.  LPC lanes of 4 states per channel; the state is read and written once.
@@ -234,8 +221,9 @@ hipError_t fwd_cfg(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
         hipLaunchKernelGGL((scan_fwd_kernel<T, SP, SCALAR, true>), dim3((waves * (p.nseg - 1) + wpg - 1) / wpg), block, 0, st,
                            a, p);
         const size_t n = static_cast<size_t>(a.B) * a.D * a.S;
-        hipLaunchKernelGGL(scan_compose_kernel, dim3(static_cast<unsigned>((n + kScanThreads - 1) / kScanThreads)), block, 0,
-                           st, a, p);
+        const int waves = compose_waves(p.nseg);
+        hipLaunchKernelGGL(waves > 1 ? scan_compose_kernel<kComposeWaves> : scan_compose_kernel<1>,
+                           dim3(static_cast<unsigned>((n + 63) / 64)), dim3(64 * waves), 0, st, a, p);
     }
     ProfScope prof(kProfSelScan, st);
     hipLaunchKernelGGL((scan_fwd_kernel<T, SP, SCALAR, false>), dim3((waves * p.nseg + wpg - 1) / wpg), block, 0, st, a, p);
@@ -275,10 +263,13 @@ hipError_t step_typed(const ScanArgs& a, hipStream_t st) {
 ScanPlan scan_fwd_plan(int B, int N, int D, int G, int S) {
     ScanPlan p{};
     p.nblk = G * ((D / G + 63) / 64);
-    // Segments: as many as bring the chip four waves a SIMD, of 64 tokens at least.
+    // Segments: as many as bring the chip four waves a SIMD, of 16 tokens at least (a wave takes
+    // 0.4 us a token where it has its SIMD to itself: 512 tokens of 2048 channels run 50 us
+    // in segments of 64 tokens, 26 us in segments of 16).  Below 64 tokens the launches of a
+    // cut cost more than it saves (32 tokens of 2048 channels 18 us whole, 24 us cut).
     const size_t waves = static_cast<size_t>(p.nblk) * (B > 0 ? B : 1);
     int want = waves >= 2048 ? 1 : static_cast<int>((4096 + waves - 1) / waves);
-    const int most = N / 64 > 1 ? N / 64 : 1;
+    const int most = N >= 64 ? N / 16 : 1;
     if (want > most) want = most;
     const int steps = (N + kAhead - 1) / kAhead, per = (steps + want - 1) / want;
     p.seg = per > 0 ? per * kAhead : kAhead;

@@ -238,47 +238,23 @@ __global__ __launch_bounds__(kScanThreads) void scan_first_kernel(ScanArgs a, Sc
 }
 
 // Entry states (in place of the end states) and, behind each segment, the adjoint (in place
-// of the one that the next segment lets out of its front).
-__global__ __launch_bounds__(kScanThreads) void scan_compose_both_kernel(ScanArgs a, ScanPlan pl) {
-    const size_t ds = static_cast<size_t>(a.D) * a.S, id = static_cast<size_t>(blockIdx.x) * kScanThreads + threadIdx.x;
-    if (id >= ds * a.B) return;
-    const size_t b = id / ds, e = id % ds;
+// of the one that it lets out of its front).
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void scan_compose_both_kernel(ScanArgs a, ScanPlan pl) {
+    __shared__ ComposeSums<WAVES> sums;
+    const size_t ds = static_cast<size_t>(a.D) * a.S, id = static_cast<size_t>(blockIdx.x) * 64 + (threadIdx.x & 63);
+    // The last workgroup's idle lanes walk no segment: the walk is in place, and a pair has one owner.
+    const bool live = id < ds * a.B;
+    const size_t in = live ? id : 0;
+    const int nseg = live ? pl.nseg : 0;
+    const size_t b = in / ds, e = in % ds;
     const float A2 = a.A[e] * kLog2e;
-    float* end = a.workspace + pl.off_end + b * pl.nseg * ds + e;
-    float* rev = a.workspace + pl.off_rev + b * pl.nseg * ds + e;
     const float* sum = a.workspace + pl.off_dt + b * pl.nseg * a.D + e / a.S;
-    constexpr int U = 8;           // segments whose loads are in flight together
-    float own[U], dec[U];
-    float h = a.state_in != nullptr ? a.state_in[id] : 0.f;
-    for (int s0 = 0; s0 < pl.nseg; s0 += U) {
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int s = s0 + k < pl.nseg ? s0 + k : pl.nseg - 1;
-            own[k] = end[s * ds];
-            dec[k] = exp2_fast(A2 * sum[static_cast<size_t>(s) * a.D]);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (s0 + k >= pl.nseg) break;
-            end[(s0 + k) * ds] = h;
-            h = fmaf(dec[k], h, own[k]);
-        }
-    }
-    float w = a.gstate_out != nullptr ? a.gstate_out[id] : 0.f;
-    for (int s0 = pl.nseg - 1; s0 >= 0; s0 -= U) {
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int s = s0 - k > 0 ? s0 - k : 0;
-            own[k] = s > 0 ? rev[s * ds] : 0.f;      // the first segment's would go to grad_state_in
-            dec[k] = exp2_fast(A2 * sum[static_cast<size_t>(s) * a.D]);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (s0 - k < 0) break;
-            rev[(s0 - k) * ds] = w;
-            w = fmaf(dec[k], w, own[k]);
-        }
-    }
+    compose<WAVES, false>(a.workspace + pl.off_end + b * pl.nseg * ds + e, sum, ds, a.D, nseg, A2,
+                          a.state_in != nullptr ? a.state_in[in] : 0.f, sums);
+    __syncthreads();
+    compose<WAVES, true>(a.workspace + pl.off_rev + b * pl.nseg * ds + e, sum, ds, a.D, nseg, A2,
+                         a.gstate_out != nullptr ? a.gstate_out[in] : 0.f, sums);
 }
 
 // Lanes of the main pass: LPC adjacent lanes hold one channel's states.  With LPC = 4 the state
@@ -686,8 +662,9 @@ hipError_t first_passes(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
                        p);
     if (p.nseg > 1) {
         const size_t n = static_cast<size_t>(a.B) * a.D * a.S;
-        hipLaunchKernelGGL(scan_compose_both_kernel, dim3(static_cast<unsigned>((n + kScanThreads - 1) / kScanThreads)), block,
-                           0, st, a, p);
+        const int waves = compose_waves(p.nseg);
+        hipLaunchKernelGGL(waves > 1 ? scan_compose_both_kernel<kComposeWaves> : scan_compose_both_kernel<1>,
+                           dim3(static_cast<unsigned>((n + 63) / 64)), dim3(64 * waves), 0, st, a, p);
     }
     return hipGetLastError();
 }
@@ -732,10 +709,10 @@ ScanPlan scan_bwd_plan(int B, int N, int D, int G, int S) {
     ScanPlan p{};
     const int ch = S <= 16 ? 64 : S <= 32 ? 32 : 16;       // channels of a workgroup of the main pass
     p.nblk = G * ((D / G + ch - 1) / ch);
-    // Segments: as many as bring the chip four waves of the first passes a SIMD, of 4 tiles at
+    // Segments: as many as bring the chip two waves of either first pass a SIMD, of a tile at
     // least.
     const size_t waves = static_cast<size_t>(G) * ((D / G + 63) / 64) * (B > 0 ? B : 1);
-    const int most = N / (4 * kTile) > 1 ? N / (4 * kTile) : 1;
+    const int most = N / kTile > 1 ? N / kTile : 1;
     int want = waves >= 2048 ? 1 : static_cast<int>((kWantWaves + waves - 1) / waves);
     if (want > most) want = most;
     const int steps = (N + kTile - 1) / kTile, per = (steps + want - 1) / want;

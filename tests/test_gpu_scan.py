@@ -5,7 +5,10 @@ adds one term of 12 roundings (softplus, two products); what is left of a state 
 of |dt A| reached L is e^-L of it, and L e^-L <= 0.4, so N steps are off by at most 8 N u
 relative to the recurrence over absolute values, plus the read-out's sum over S states and the
 gate: k = 8 N + 4 S + 64.  Backward: the same once more for the adjoint, and sums over 64
-channels and their blocks, or over tokens: k = 20 N + 8 S + 256.
+channels and their blocks, or over tokens: k = 20 N + 8 S + 256.  The gate's derivative
+s + z s (1 - s) crosses zero at z = -1.2785, where its two terms are 0.218 each and the
+roundings of both stay: its magnitude is the sum of theirs, not |their sum| (at z = -1.278493
+that sum is 6e-6, and half a step of 0.218 already 2e-3 of it).
 """
 import numpy as np
 import pytest
