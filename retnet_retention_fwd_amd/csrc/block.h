@@ -40,7 +40,7 @@ struct NormArgs {
 };
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t stream);
-size_t norm_bwd_workspace(size_t rows, int D, bool bf16);
+size_t norm_bwd_workspace(size_t rows, int D);
 
 // Rotary positions (rotary.hip).
 struct RotaryView {

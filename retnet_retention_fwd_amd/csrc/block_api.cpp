@@ -233,7 +233,7 @@ retn_status layer_norm_fwd(const void* x, const void* weight, const void* bias, 
 
 size_t layer_norm_bwd_workspace_bytes(long long rows, int D, retn_dtype dtype) {
     if (!valid_dtype(dtype) || norm_sizes(rows, D) != RETN_OK) return 0;
-    return retn::norm_bwd_workspace(sz(rows), D, dtype == RETN_BF16);
+    return retn::norm_bwd_workspace(sz(rows), D);
 }
 
 retn_status layer_norm_bwd(const void* x, const void* weight, const float* mean, const float* rstd, const void* grad_y,

@@ -146,9 +146,10 @@ __device__ __forceinline__ void store_state(float* p, int S, const float (&h)[SP
 // being what it makes of a zero state: `at` holds own and gets e.  A lane takes a (channel,
 // state) pair.  WAVES = 1: it walks all segments, for there are few of them and many pairs.
 // Otherwise the waves of a workgroup share 64 pairs' segments: each composes its own from
-// zero, then all of those before it, then walks its own again.  Pre-pass and composition of
-// a forward, S = 16, bf16, in us with 1 and 16 waves: 16 segments of 524288 pairs 67 and 99, 32 of
-// 131072 67 and 77, 64 of 65536 30 and 32, 128 of 16384 32 and 23, 1024 of 2048 112 and 39.
+// zero, then all of those before it, then walks its own again.  First passes and composition,
+// S = 16, bf16, in us with 1 and 16 waves: forward, 16 segments of 524288 pairs 67 and 99,
+// 32 of 131072 67 and 77, 64 of 65536 30 and 32, 128 of 16384 32 and 23, 1024 of 2048 112 and
+// 39; backward, 32 of 65536 46 and 50, 64 of 32768 76 and 70.
 constexpr int kComposeWaves = 16;
 template <int WAVES>
 struct ComposeSums {
@@ -198,7 +199,7 @@ __device__ __forceinline__ void compose(float* at, const float* sum, size_t ds, 
         }
     }
 }
-inline int compose_waves(int nseg) { return nseg > 4 * kComposeWaves ? kComposeWaves : 1; }
+inline int compose_waves(int nseg) { return nseg > 3 * kComposeWaves ? kComposeWaves : 1; }
 
 // Whether B's and C's rows can be read by scalar loads (WaveRow).
 inline bool scalar_rows(const ScanArgs& a, int SP) {
