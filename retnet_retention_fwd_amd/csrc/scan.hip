@@ -22,9 +22,11 @@ namespace retn {
 
 namespace {
 
-// STATE: the first pass of a segmented sequence, no y.
+// STATE: the first pass of a segmented sequence, no y.  (With the register limits the matrix
+// instructions' states are in vector registers; without, they move to accumulation
+// registers and back for every product: 153 us where these take 128.)
 template <typename T, int SP, bool SCALAR, bool STATE>
-__global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, ScanPlan pl) {
+__global__ __launch_bounds__(kScanThreads, SP <= 16 ? 4 : 2) void scan_fwd_kernel(ScanArgs a, ScanPlan pl) {
     const unsigned id = wave_id();
     const int nseg = STATE ? pl.nseg - 1 : pl.nseg;
     if (id >= static_cast<unsigned>(pl.nblk) * nseg * a.B) return;
@@ -32,7 +34,11 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
     const int c = p.c0 + (threadIdx.x & 63), S = SCALAR ? SP : a.S;
     const bool on = c < p.cend;
     const int ch = on ? c : p.cend - 1;        // idle lanes repeat the last channel and store nothing
-    float A2[SP], h[SP];
+    using Rows = MatRows<T, SP>;
+    using Block = MatBlock<T, SP>;
+    using Read = WaveRow<T, SP, SCALAR>;
+    float A2[SP], first[SP];
+    f32v4 h[SP / 4];
     load_state<SP>(a.A + static_cast<size_t>(ch) * S, S, true, A2);
 #pragma unroll
     for (int i = 0; i < SP; ++i) A2[i] *= kLog2e;
@@ -41,7 +47,9 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
     const float* from = STATE ? nullptr : pl.nseg > 1 ? a.workspace + pl.off_end + slot * S
                         : a.state_in != nullptr       ? a.state_in + bd * S
                                                       : nullptr;
-    load_state<SP>(from, S, from != nullptr, h);
+    load_state<SP>(from, S, from != nullptr, first);
+#pragma unroll
+    for (int i = 0; i < SP; ++i) h[i / 4][i % 4] = first[i];
     const float bias = a.bias != nullptr ? a.bias[ch] : 0.f, skip = a.Dskip != nullptr ? a.Dskip[ch] : 0.f;
     float dsum = 0.f;
     const size_t tok0 = static_cast<size_t>(p.b) * a.N;
@@ -56,13 +64,19 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
     const bool gated = !STATE && a.z != nullptr;
 
     // one token's step of all states; its read-out
-    auto step = [&](float dt, float x, const WaveRow<T, SP, SCALAR>& B, const WaveRow<T, SP, SCALAR>& C) {
+    auto step = [&](float dt, float x, float B, auto tok, const Read& C) __attribute__((always_inline)) {
         const float u = dt * x;
         float y0 = skip * x, y1 = 0.f;
+        each<SP / 4>([&](auto j) __attribute__((always_inline)) {
+            f32v4 d;
 #pragma unroll
-        for (int i = 0; i < SP; ++i) {
-            h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], u * B.get(i));
-            if (!STATE) (i & 1 ? y1 : y0) = fmaf(C.get(i), h[i], i & 1 ? y1 : y0);
+            for (int i = 0; i < 4; ++i) d[i] = exp2_fast(dt * A2[4 * j + i]) * h[j][i];
+            h[j] = outer<SP, tok, j>(B, u, d);
+        });
+        if constexpr (!STATE) {
+            each<SP>([&](auto i) __attribute__((always_inline)) {
+                (i & 1 ? y1 : y0) = fmaf(C.template get<i>(S), h[i / 4][i % 4], i & 1 ? y1 : y0);
+            });
         }
         dsum += dt;
         return y0 + y1;
@@ -70,6 +84,9 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
     auto gate = [&](float z) { return z * sigmoid_f(z); };
 
     T rx[kAhead], rdt[kAhead], rz[kAhead] = {};
+    Block rB;
+    Read rC[kAhead];                           // not SCALAR
+    const uint32_t row_lane = Rows::lane_at(a.ldb, S), row_one = Rows::lane_at(0, S);
     auto fetch = [&](int t0) {
         const long long ldx = stepped(a.ldx), lddt = stepped(a.lddt), ldz = stepped(a.ldz);
         const uint32_t lane = opaque(at);      // added last, by the load itself
@@ -90,6 +107,16 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
                 zr += ldz;
             }
         }
+        rB.load(Bp + t0 * a.ldb, a.ldb, row_lane);
+        if (!STATE && !SCALAR) {
+            const long long ldc = stepped(a.ldc);
+            const T* cr = Cp + t0 * ldc;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                rC[k].load(cr, S);
+                cr += ldc;
+            }
+        }
     };
     int t = p.t_begin;
     if (t + kAhead <= p.t_end) fetch(t);
@@ -97,33 +124,32 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
         // the block's steps and, behind them, its gates are taken together, so that the tokens
         // between them are straight code
         float x[kAhead], dt[kAhead], z[kAhead], y[kAhead];
-        WaveRow<T, SP, SCALAR> B[2], C[2];
-        const long long ldb = stepped(a.ldb), ldc = stepped(a.ldc);
-        const T* Bt = Bp + t * ldb;
+        float B[Block::kRegs];
+        rB.values(S, B);
+        Read C[SCALAR ? 2 : kAhead];
+        const long long ldc = stepped(a.ldc);
         const T* Ct = Cp + t * ldc;
-        B[0].load(Bt, S);
-        if (!STATE) C[0].load(Ct, S);
+        if (!STATE && SCALAR) C[0].load(Ct, S);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             x[k] = up(rx[k]);
             dt[k] = up(rdt[k]) + bias;
             z[k] = up(rz[k]);
+            if (!STATE && !SCALAR) C[k] = rC[k];
         }
         if (t + 2 * kAhead <= p.t_end) fetch(t + kAhead);
         if (a.softplus) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) dt[k] = softplus_f(dt[k]);
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            rows_arrived<SCALAR>();
-            if (k + 1 < kAhead) {
-                B[(k + 1) & 1].load(Bt += ldb, S);
-                if (!STATE) C[(k + 1) & 1].load(Ct += ldc, S);
+        each<kAhead>([&](auto k) __attribute__((always_inline)) {
+            if (!STATE && SCALAR) {
+                rows_arrived();
+                if (k + 1 < kAhead) C[(k + 1) & 1].load(Ct += ldc, S);
+                rows_issued();
             }
-            rows_issued<SCALAR>();
-            y[k] = step(dt[k], x[k], B[k & 1], C[k & 1]);
-        }
+            y[k] = step(dt[k], x[k], B[k / Block::kTok], std::integral_constant<int, k % Block::kTok>{}, C[SCALAR ? k & 1 : k]);
+        });
         if (STATE) continue;
         if (gated) {
 #pragma unroll
@@ -141,21 +167,24 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a, Scan
         }
     }
     for (; t < p.t_end; ++t) {
-        WaveRow<T, SP, SCALAR> B, C;
-        B.load(Bp + static_cast<size_t>(t) * a.ldb, S);
+        Read C;
         if (!STATE) C.load(Cp + static_cast<size_t>(t) * a.ldc, S);
         const size_t tt = t;
-        float y = step(step_size(up(row_at(dp + tt * a.lddt, at)) + bias, a.softplus), up(row_at(xp + tt * a.ldx, at)), B, C);
+        const float B = Rows::value(row_at(Bp + tt * a.ldb, row_one), S);   // every token's lanes: this one
+        float y = step(step_size(up(row_at(dp + tt * a.lddt, at)) + bias, a.softplus), up(row_at(xp + tt * a.ldx, at)), B,
+                       std::integral_constant<int, 0>{}, C);
         if (STATE) continue;
         if (gated) y *= gate(up(row_at(zp + tt * a.ldz, at)));
         if (on) row_put(yp + tt * a.D, at, down<T>(y));
     }
     if (!on) return;
+#pragma unroll
+    for (int i = 0; i < SP; ++i) first[i] = h[i / 4][i % 4];
     if (STATE) {
-        store_state<SP>(a.workspace + pl.off_end + slot * S, S, h);
+        store_state<SP>(a.workspace + pl.off_end + slot * S, S, first);
         a.workspace[pl.off_dt + slot] = dsum;
     } else if (p.seg == pl.nseg - 1 && a.state_out != nullptr) {
-        store_state<SP>(a.state_out + bd * S, S, h);
+        store_state<SP>(a.state_out + bd * S, S, first);
     }
 }
 
@@ -226,7 +255,7 @@ hipError_t fwd_cfg(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
         hipLaunchKernelGGL((scan_fwd_kernel<T, SP, SCALAR, true>), dim3((waves * (p.nseg - 1) + wpg - 1) / wpg), block, 0, st,
                            a, p);
         const size_t n = static_cast<size_t>(a.B) * a.D * a.S;
-        const int waves = compose_waves(p.nseg);
+        const int waves = compose_waves(p.nseg, n);
         hipLaunchKernelGGL(waves > 1 ? scan_compose_kernel<kComposeWaves> : scan_compose_kernel<1>,
                            dim3(static_cast<unsigned>((n + 63) / 64)), dim3(64 * waves), 0, st, a, p);
     }

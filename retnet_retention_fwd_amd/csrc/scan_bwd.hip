@@ -41,18 +41,20 @@ constexpr int SPL = 4;         // states of a lane in the main pass
 
 // The state in front of each tile, its segment walked from zero, and the sum of dt from the
 // segment's first token to there; the end state and whole sum of dt go to the segment's slot.
-template <typename T, int SP, bool SCALAR>
+template <typename T, int SP, bool ALL>
 __device__ __forceinline__ void keep_states(const ScanArgs& a, const ScanPlan& pl, int nblk, unsigned id) {
     const ScanPlace p = scan_place<64>(a, nblk, pl.nseg, pl.seg, id);
-    const int c = p.c0 + (threadIdx.x & 63), S = SCALAR ? SP : a.S;
+    const int c = p.c0 + (threadIdx.x & 63), S = ALL ? SP : a.S;
     const bool on = c < p.cend;
     const int ch = on ? c : p.cend - 1;
-    float A2[SP], h[SP], dsum = 0.f;
+    using Block = MatBlock<T, SP>;
+    float A2[SP], dsum = 0.f;
+    f32v4 h[SP / 4];
     load_state<SP>(a.A + static_cast<size_t>(ch) * S, S, true, A2);
 #pragma unroll
     for (int i = 0; i < SP; ++i) {
         A2[i] *= kLog2e;
-        h[i] = 0.f;
+        h[i / 4][i % 4] = 0.f;
     }
     const int tiles = (a.N + kTile - 1) / kTile;
     const float bias = a.bias != nullptr ? a.bias[ch] : 0.f;
@@ -61,19 +63,31 @@ __device__ __forceinline__ void keep_states(const ScanArgs& a, const ScanPlan& p
     const T* dp = static_cast<const T*>(a.dt) + tok0 * a.lddt;
     const uint32_t lane_at = static_cast<uint32_t>(ch) * sizeof(T);
     const T* Bp = static_cast<const T*>(a.Bm) + tok0 * a.ldb + p.g * S;
-    auto step = [&](float dt, float x, const WaveRow<T, SP, SCALAR>& B) {
+    const uint32_t row_lane = MatRows<T, SP>::lane_at(a.ldb, S), row_one = MatRows<T, SP>::lane_at(0, S);
+    auto step = [&](float dt, float x, float B, auto tok) __attribute__((always_inline)) {
         const float u = dt * x;
+        each<SP / 4>([&](auto j) __attribute__((always_inline)) {
+            f32v4 d;
 #pragma unroll
-        for (int i = 0; i < SP; ++i) h[i] = fmaf(exp2_fast(dt * A2[i]), h[i], u * B.get(i));
+            for (int i = 0; i < 4; ++i) d[i] = exp2_fast(dt * A2[4 * j + i]) * h[j][i];
+            h[j] = outer<SP, tok, j>(B, u, d);
+        });
         dsum += dt;
+    };
+    auto put = [&](float* to) {
+        float v[SP];
+#pragma unroll
+        for (int i = 0; i < SP; ++i) v[i] = h[i / 4][i % 4];
+        store_state<SP>(to, S, v);
     };
     auto keep = [&](int t) {
         if (!on) return;
         const size_t at = (static_cast<size_t>(p.b) * tiles + t / kTile) * a.D + ch;
-        store_state<SP>(a.workspace + pl.off_ckpt + at * S, S, h);
+        put(a.workspace + pl.off_ckpt + at * S);
         a.workspace[pl.off_cum + at] = dsum;
     };
     T rx[kAhead], rdt[kAhead];
+    Block rB;
     auto fetch = [&](int t0) {
         const long long ldx = stepped(a.ldx), lddt = stepped(a.lddt);
         const uint32_t at = opaque(lane_at);   // added last, by the load itself
@@ -86,16 +100,14 @@ __device__ __forceinline__ void keep_states(const ScanArgs& a, const ScanPlan& p
             xr += ldx;
             dr += lddt;
         }
+        rB.load(Bp + t0 * a.ldb, a.ldb, row_lane);
     };
     int t = p.t_begin;
     if (t + kAhead <= p.t_end) fetch(t);
     for (; t + kAhead <= p.t_end; t += kAhead) {
         if (t % kTile == 0) keep(t);
-        float x[kAhead], dt[kAhead];
-        WaveRow<T, SP, SCALAR> B[2];
-        const long long ldb = stepped(a.ldb);
-        const T* Bt = Bp + t * ldb;
-        B[0].load(Bt, S);
+        float x[kAhead], dt[kAhead], B[Block::kRegs];
+        rB.values(S, B);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             x[k] = up(rx[k]);
@@ -106,29 +118,25 @@ __device__ __forceinline__ void keep_states(const ScanArgs& a, const ScanPlan& p
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) dt[k] = softplus_f(dt[k]);
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            rows_arrived<SCALAR>();
-            if (k + 1 < kAhead) B[(k + 1) & 1].load(Bt += ldb, S);
-            rows_issued<SCALAR>();
-            step(dt[k], x[k], B[k & 1]);
-        }
+        each<kAhead>([&](auto k) __attribute__((always_inline)) {
+            step(dt[k], x[k], B[k / Block::kTok], std::integral_constant<int, k % Block::kTok>{});
+        });
     }
     for (; t < p.t_end; ++t) {
         if (t % kTile == 0) keep(t);
-        WaveRow<T, SP, SCALAR> B;
-        B.load(Bp + static_cast<size_t>(t) * a.ldb, S);
         const size_t tt = t;
-        step(step_size(up(row_at(dp + tt * a.lddt, lane_at)) + bias, a.softplus), up(row_at(xp + tt * a.ldx, lane_at)), B);
+        const float B = MatRows<T, SP>::value(row_at(Bp + tt * a.ldb, row_one), S);
+        step(step_size(up(row_at(dp + tt * a.lddt, lane_at)) + bias, a.softplus), up(row_at(xp + tt * a.ldx, lane_at)), B,
+             std::integral_constant<int, 0>{});
     }
     if (!on || pl.nseg == 1) return;
     const size_t slot = (static_cast<size_t>(p.b) * pl.nseg + p.seg) * a.D + ch;
-    store_state<SP>(a.workspace + pl.off_end + slot * S, S, h);
+    put(a.workspace + pl.off_end + slot * S);
     a.workspace[pl.off_dt + slot] = dsum;
 }
 
 // The adjoint that leaves each segment but the first at its front, from zero behind its end.
-template <typename T, int SP, bool SCALAR>
+template <typename T, int SP, bool ALL>
 __device__ __forceinline__ void walk_back(const ScanArgs& a, const ScanPlan& pl, int nblk, unsigned id) {
     ScanPlace p = scan_place<64>(a, nblk, pl.nseg - 1, pl.seg, id);
     p.seg += 1;                                // the place of the segment behind
@@ -136,15 +144,17 @@ __device__ __forceinline__ void walk_back(const ScanArgs& a, const ScanPlan& pl,
     p.t_full = p.t_begin + pl.seg < a.N ? p.t_begin + pl.seg : a.N;
     const int n = scan_length(a.lengths, p.b, a.N);
     p.t_end = p.t_full < n ? p.t_full : n;
-    const int c = p.c0 + (threadIdx.x & 63), S = SCALAR ? SP : a.S;
+    const int c = p.c0 + (threadIdx.x & 63), S = ALL ? SP : a.S;
     const bool on = c < p.cend;
     const int ch = on ? c : p.cend - 1;
-    float A2[SP], w[SP];
+    using Block = MatBlock<T, SP>;
+    float A2[SP];
+    f32v4 w[SP / 4];
     load_state<SP>(a.A + static_cast<size_t>(ch) * S, S, true, A2);
 #pragma unroll
     for (int i = 0; i < SP; ++i) {
         A2[i] *= kLog2e;
-        w[i] = 0.f;
+        w[i / 4][i % 4] = 0.f;
     }
     const float bias = a.bias != nullptr ? a.bias[ch] : 0.f;
     const size_t tok0 = static_cast<size_t>(p.b) * a.N;
@@ -154,23 +164,27 @@ __device__ __forceinline__ void walk_back(const ScanArgs& a, const ScanPlan& pl,
     const uint32_t lane_at = static_cast<uint32_t>(ch) * sizeof(T);
     const T* Cp = static_cast<const T*>(a.Cm) + tok0 * a.ldc + p.g * S;
     const bool gated = a.z != nullptr;
-    auto step = [&](float dt, float g, const WaveRow<T, SP, SCALAR>& C) {
+    const uint32_t row_lane = MatRows<T, SP>::lane_at(a.ldc, S), row_one = MatRows<T, SP>::lane_at(0, S);
+    auto step = [&](float dt, float g, float C, auto tok) __attribute__((always_inline)) {
+        each<SP / 4>([&](auto j) __attribute__((always_inline)) {
+            w[j] = outer<SP, tok, j>(C, g, w[j]);
 #pragma unroll
-        for (int i = 0; i < SP; ++i) w[i] = exp2_fast(dt * A2[i]) * fmaf(C.get(i), g, w[i]);
+            for (int i = 0; i < 4; ++i) w[j][i] *= exp2_fast(dt * A2[4 * j + i]);
+        });
     };
     const int blocks = p.t_end > p.t_begin ? (p.t_end - p.t_begin) / kAhead : 0;
     for (int t = p.t_end - 1; t >= p.t_begin + blocks * kAhead; --t) {
-        WaveRow<T, SP, SCALAR> C;
-        C.load(Cp + static_cast<size_t>(t) * a.ldc, S);
         const size_t tt = t;
+        const float C = MatRows<T, SP>::value(row_at(Cp + tt * a.ldc, row_one), S);
         float g = up(row_at(gp + tt * a.D, lane_at));
         if (gated) {
             const float z = up(row_at(zp + tt * a.ldz, lane_at));
             g *= z * sigmoid_f(z);
         }
-        step(step_size(up(row_at(dp + tt * a.lddt, lane_at)) + bias, a.softplus), g, C);
+        step(step_size(up(row_at(dp + tt * a.lddt, lane_at)) + bias, a.softplus), g, C, std::integral_constant<int, 0>{});
     }
     T rdt[kAhead], rz[kAhead] = {}, rg[kAhead];
+    Block rC;
     auto fetch = [&](int t0) {
         const long long lddt = stepped(a.lddt), ldg = stepped(a.D), ldz = stepped(a.ldz);
         const uint32_t at = opaque(lane_at);
@@ -191,15 +205,13 @@ __device__ __forceinline__ void walk_back(const ScanArgs& a, const ScanPlan& pl,
                 zr += ldz;
             }
         }
+        rC.load(Cp + t0 * a.ldc, a.ldc, row_lane);
     };
     if (blocks > 0) fetch(p.t_begin + (blocks - 1) * kAhead);
     for (int blk = blocks - 1; blk >= 0; --blk) {
         const int t = p.t_begin + blk * kAhead;
-        float dt[kAhead], g[kAhead], z[kAhead];
-        WaveRow<T, SP, SCALAR> C[2];
-        const long long ldc = stepped(a.ldc);
-        const T* Ct = Cp + (t + kAhead - 1) * ldc;
-        C[(kAhead - 1) & 1].load(Ct, S);
+        float dt[kAhead], g[kAhead], z[kAhead], C[Block::kRegs];
+        rC.values(S, C);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             dt[k] = up(rdt[k]) + bias;
@@ -215,31 +227,32 @@ __device__ __forceinline__ void walk_back(const ScanArgs& a, const ScanPlan& pl,
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) g[k] *= z[k] * sigmoid_f(z[k]);
         }
-#pragma unroll
-        for (int k = kAhead - 1; k >= 0; --k) {
-            rows_arrived<SCALAR>();
-            if (k > 0) C[(k - 1) & 1].load(Ct -= ldc, S);
-            rows_issued<SCALAR>();
-            step(dt[k], g[k], C[k & 1]);
-        }
+        each<kAhead>([&](auto i) __attribute__((always_inline)) {
+            constexpr int k = kAhead - 1 - i;
+            step(dt[k], g[k], C[k / Block::kTok], std::integral_constant<int, k % Block::kTok>{});
+        });
     }
     if (!on) return;
     const size_t slot = (static_cast<size_t>(p.b) * pl.nseg + p.seg) * a.D + ch;
-    store_state<SP>(a.workspace + pl.off_rev + slot * S, S, w);
+    float out[SP];
+#pragma unroll
+    for (int i = 0; i < SP; ++i) out[i] = w[i / 4][i % 4];
+    store_state<SP>(a.workspace + pl.off_rev + slot * S, S, out);
 }
 
 // Both walks in one launch: neither needs the other, and together they bring each SIMD the
 // waves that keep its vector ALU busy (142 us one behind the other in a training step's
 // backward, 120 us together, with the composition).
-template <typename T, int SP, bool SCALAR>
-__global__ __launch_bounds__(kScanThreads) void scan_first_kernel(ScanArgs a, ScanPlan pl) {
+// ALL: S = SP; its rows are then stored without tests (4 x 2048 x 512 channels, S = 64: 133 us against 165).
+template <typename T, int SP, bool ALL>
+__global__ __launch_bounds__(kScanThreads, SP <= 16 ? 4 : 2) void scan_first_kernel(ScanArgs a, ScanPlan pl) {
     const unsigned id = wave_id();
     const int nblk = a.G * ((a.D / a.G + 63) / 64);
     const unsigned one = static_cast<unsigned>(nblk) * a.B, forward = one * pl.nseg;
     if (id < forward)
-        keep_states<T, SP, SCALAR>(a, pl, nblk, id);
+        keep_states<T, SP, ALL>(a, pl, nblk, id);
     else if (id - forward < one * (pl.nseg - 1))
-        walk_back<T, SP, SCALAR>(a, pl, nblk, id - forward);
+        walk_back<T, SP, ALL>(a, pl, nblk, id - forward);
 }
 
 // Entry states (in place of the end states) and, behind each segment, the adjoint (in place
@@ -658,17 +671,20 @@ __global__ __launch_bounds__(kScanThreads) void scan_bc_kernel(ScanArgs a, ScanP
     static_cast<T*>(id < one ? a.gB : a.gC)[e] = down<T>(t);
 }
 
-template <typename T, int SP, bool SCALAR>
+template <typename T, int SP>
 hipError_t first_passes(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
     const dim3 block(kScanThreads);
     constexpr unsigned wpg = kScanThreads / 64;
     const unsigned waves = static_cast<unsigned>(a.G * ((a.D / a.G + 63) / 64)) * a.B;
     ProfScope prof(kProfScanPre, st);
-    hipLaunchKernelGGL((scan_first_kernel<T, SP, SCALAR>), dim3((waves * (2 * p.nseg - 1) + wpg - 1) / wpg), block, 0, st, a,
-                       p);
+    const dim3 grid((waves * (2 * p.nseg - 1) + wpg - 1) / wpg);
+    if (a.S == SP)
+        hipLaunchKernelGGL((scan_first_kernel<T, SP, true>), grid, block, 0, st, a, p);
+    else
+        hipLaunchKernelGGL((scan_first_kernel<T, SP, false>), grid, block, 0, st, a, p);
     if (p.nseg > 1) {
         const size_t n = static_cast<size_t>(a.B) * a.D * a.S;
-        const int waves = compose_waves(p.nseg);
+        const int waves = compose_waves(p.nseg, n);
         hipLaunchKernelGGL(waves > 1 ? scan_compose_both_kernel<kComposeWaves> : scan_compose_both_kernel<1>,
                            dim3(static_cast<unsigned>((n + 63) / 64)), dim3(64 * waves), 0, st, a, p);
     }
@@ -681,7 +697,7 @@ hipError_t bwd_states(const ScanArgs& a, const ScanPlan& p, hipStream_t st) {
     const dim3 block(kScanThreads);
     const unsigned wgs = static_cast<unsigned>(p.nblk) * a.B;
     if (wgs > 0) {
-        hipError_t e = scalar_rows(a, SP) ? first_passes<T, SP, true>(a, p, st) : first_passes<T, SP, false>(a, p, st);
+        hipError_t e = first_passes<T, SP>(a, p, st);
         if (e != hipSuccess) return e;
         {
             ProfScope prof(kProfSelScan, st);
