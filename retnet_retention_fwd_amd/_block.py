@@ -116,12 +116,14 @@ def _given(t, name, dtype, dev, shape):
 def _rows(t, name, dtype, dev, shape, inner=1):
     """A [B, N, ...] (or [B, ...]) tensor whose tokens lie one stride apart; its `inner` last
     axes are contiguous.  Returns that stride."""
-    if dev is not None:
-        try:
-            if t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
-                return shape[-1] if inner == 1 else shape[-1] * shape[-2]
-        except AttributeError:
-            pass
+    try:       # contiguous, as a rule
+        if dev is None:
+            if inner == 1 and dtype is None and shape is None and t.is_contiguous() and t.get_device() >= 0 and t.dim() > 1:
+                return t.shape[-1]
+        elif t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
+            return shape[-1] if inner == 1 else shape[-1] * shape[-2]
+    except AttributeError:
+        pass
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -333,13 +335,13 @@ def _rotary(fn, q, k, table, positions, offset, interleaved, q_scale, k_scale, o
     on, s = _on(dev, stream)
     with on:
         if out_q is None:
-            out_q = torch.empty((B, Hq, N, d), dtype=t, device=dev)
+            out_q = q.new_empty((B, Hq, N, d))
             soq = (Hq * N * d, N * d, d)
         else:
             soq = _heads(out_q, "out_q", t, dev, q.shape)
         if k is not None:
             if out_k is None:
-                out_k = torch.empty((B, Hk, N, d), dtype=t, device=dev)
+                out_k = k.new_empty((B, Hk, N, d))
                 sok = (Hk * N * d, N * d, d)
             else:
                 sok = _heads(out_k, "out_k", t, dev, k.shape)
@@ -434,7 +436,7 @@ def causal_conv_step(x, weight, state, bias=None, silu=False, out=None, stream=N
     on, s = _on(dev, stream)
     with on:
         _given(out, "out", x.dtype, dev, (B, D))
-        y = torch.empty((B, D), dtype=x.dtype, device=dev) if out is None else out
+        y = x.new_empty((B, D)) if out is None else out
         _check(_fn("causal_conv_step")(_ptr(x), ldx, _ptr(weight), _ptr(bias), _ptr(state), _ptr(y), B, D, K,
                                        int(bool(silu)), code, wcode, s), "causal_conv_step")
     return y
@@ -447,14 +449,15 @@ def _scan_shapes(x, dt, A, Bm, Cm, D, z, dt_bias, step):
     ldx = _rows(x, "x", None, None, None)
     if x.dim() != (2 if step else 3):
         raise ValueError("x must be " + ("[B,D]" if step else "[B,N,D]"))
-    dev, t, lead, ch = x.device, x.dtype, tuple(x.shape[:-1]), x.shape[-1]
-    code = _code(x)
-    lddt = _rows(dt, "dt", t, dev, x.shape)
-    ldz = _rows(z, "z", t, dev, x.shape) if z is not None else 0
-    _require(A, "A", torch.float32, dev)
-    if A.dim() != 2 or A.shape[0] != ch:
+    dev, t, shape = x.device, x.dtype, tuple(x.shape)
+    lead, ch, code = shape[:-1], shape[-1], _code(x)
+    lddt = _rows(dt, "dt", t, dev, shape)
+    ldz = _rows(z, "z", t, dev, shape) if z is not None else 0
+    if not isinstance(A, torch.Tensor) or A.dim() != 2 or A.shape[0] != ch:
+        _require(A, "A", torch.float32, dev)
         raise ValueError(f"A must be [{ch}, S]")
     S = A.shape[1]
+    _dense(A, "A", torch.float32, dev, (ch, S))
     if not isinstance(Bm, torch.Tensor) or Bm.dim() != len(lead) + 2:
         raise ValueError("Bm must be " + ("[B,G,S]" if step else "[B,N,G,S]"))
     G = Bm.shape[-2]
@@ -544,7 +547,7 @@ def selective_scan_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, s
     on, s = _on(dev, stream)
     with on:
         _given(out, "out", x.dtype, dev, (B, ch))
-        y = torch.empty((B, ch), dtype=x.dtype, device=dev) if out is None else out
+        y = x.new_empty((B, ch)) if out is None else out
         _check(_fn("selective_scan_step")(_ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
                                           _ptr(dt_bias), _ptr(state), _ptr(y), *ld, B, ch, G, S, int(bool(softplus)),
                                           code, s), "selective_scan_step")

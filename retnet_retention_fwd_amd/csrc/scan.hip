@@ -2,7 +2,7 @@
 //     h_t[n] = exp(dt_t A[n]) h_(t-1)[n] + dt_t x_t B_t[n],
 //     y_t = (sum_n C_t[n] h_t[n] + D x_t) silu(z_t),      dt = softplus(raw + bias)
 //
-// Bound by the vector ALUs: an exponential and four multiply-adds per (token, channel,
+// Bound by the vector ALUs: an exponential and four products per (token, channel,
 // state), where HBM moves eight bytes per (token, channel).  A lane walks over the tokens of
 // one channel with all of its states in registers (scan.h).
 //
@@ -11,10 +11,11 @@
 // sum of its dt (the segment's whole decay is exp(A sum dt)), a small kernel composes the
 // entry states, and the main pass walks all segments at once.
 //
-// Measured, S = 16, bf16, gated: 4 x 2048 x 2048 channels 126 us (first pass 56, composition 9,
-// main pass 70), 1 x 16384 x 2048 230 us; the vector ALUs are busy 72-82% of the first pass
-// and 89% of the main pass.  An exponential costs as much issue time as three multiply-adds,
-// so the pass cannot be much shorter than its instructions.
+// Measured, S = 16, bf16, gated: 4 x 2048 x 2048 channels 124 us (first pass 55, composition 9,
+// main pass 71), 1 x 16384 x 2048 228 us; the vector ALUs are busy 65-74% of the first pass
+// and 81% of the main pass, and issue matrix instructions in much of the rest.  An
+// exponential costs as much issue time as three multiply-adds, so the pass cannot be much
+// shorter than its instructions.
 
 #include "scan.h"
 

@@ -254,3 +254,31 @@ def test_no_tokens():
     got = R().selective_scan_bwd(*a, cut["x"], D=t["D"], dt_bias=t["dt_bias"], state_in=t["state_in"], grad_state_out=gs,
                                  return_grad_state_in=True)
     assert not got[2].any() and not got[5].any() and not got[7].any() and torch.equal(got[8], gs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,S", [(40, 16), (300, 16), (90, 13), (50, 64)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_channels_do_not_meet(N, S, dtype, bad):
+    """A channel whose inputs are NaN or infinite leaves every other channel's results as they
+    are, bit for bit (the gradients of B, C and the sums over channels are the exception)."""
+    print(f"\n[case] scan channels {N} {S} {dtype} {bad}", flush=True)
+    B, D, G, c = 2, 70, 1, 5
+    t, _ = case(B, N, D, G, S, dtype, False, 700)
+    g, _ = draw(720, (B, N, D), dtype)
+    kw = dict(D=t["D"], z=t["z"], dt_bias=t["dt_bias"], softplus=True, state_in=t["state_in"])
+
+    def run():
+        y, h = R().selective_scan_fwd(*fwd_args(t), **kw, return_state=True)
+        b = R().selective_scan_bwd(*fwd_args(t), g, **kw, return_grad_state_in=True)
+        return {"y": y, "state": h.transpose(1, 2), "gx": b[0], "gdt": b[1], "gA": b[2].t(), "gD": b[5], "gz": b[6],
+                "gbias": b[7], "gstate": b[8].transpose(1, 2)}
+
+    want = {n: v.clone() for n, v in run().items()}
+    t["x"][:, N // 3, c] = bad
+    got = run()
+    assert not bool(torch.isfinite(got["y"][..., c]).all())
+    for n, v in got.items():
+        w = want[n].clone()
+        w[..., c] = v[..., c] = 0
+        assert torch.equal(v, w), n
