@@ -337,8 +337,9 @@ double retention_calib_mfma_flops(int blocks, int waves, int iters);
  *              in place; other tensors are contiguous.  Any element alignment.
  *   Lengths    `lengths` (optional, [B] int32, device memory): sequence b has its first
  *              lengths[b] tokens (clamped to 0 .. N); what lies behind them is not read,
- *              output rows there are left as they were, gradient rows there are zero, and
- *              a final state is the one behind the last of those tokens.
+ *              output rows there are left as they were (the ..._fwd_padded forms write them
+ *              as zeros), gradient rows there are zero, and a final state is the one behind
+ *              the last of those tokens.
  *   Limits     D <= 2^20, B * N <= 2^31 - 2^16, B * D < 2^31, B * N * D < 2^34 (rotary:
  *              B * N * d < 2^32, Hq + Hk < 2^16), row strides < 2^26; else
  *              RETN_ERR_UNSUPPORTED.
@@ -424,6 +425,12 @@ retn_status causal_conv_fwd(const void* x, long long ldx, const void* weight, co
                             int B, int N, int D, int K, int silu, retn_dtype dtype,
                             retn_dtype wdtype, void* stream);
 
+/* causal_conv_fwd, with the rows of y behind each length written as zeros (y may be fresh memory). */
+retn_status causal_conv_fwd_padded(const void* x, long long ldx, const void* weight, const void* bias,
+                                   void* y, const void* state_in, void* state_out, const int* lengths,
+                                   int B, int N, int D, int K, int silu, retn_dtype dtype,
+                                   retn_dtype wdtype, void* stream);
+
 /*
  * Backward of causal_conv_fwd for grad_y [B, N, D] and, optionally, grad_state_out:
  * grad_x [B, N, D], and each optional: grad_weight [D, K], grad_bias [D] (of type wdtype),
@@ -469,6 +476,16 @@ retn_status selective_scan_fwd(const void* x, const void* dt, const float* A, co
                                retn_dtype dtype, void* workspace, size_t workspace_bytes,
                                void* stream);
 size_t selective_scan_workspace_bytes(int B, int N, int D, int G, int S);
+
+/* selective_scan_fwd, with the rows of y behind each length written as zeros (y may be fresh memory). */
+retn_status selective_scan_fwd_padded(const void* x, const void* dt, const float* A, const void* Bm,
+                                      const void* Cm, const float* Dskip, const void* z,
+                                      const float* dt_bias, void* y, const float* state_in,
+                                      float* state_out, const int* lengths, long long ldx,
+                                      long long lddt, long long ldz, long long ldb, long long ldc,
+                                      int B, int N, int D, int G, int S, int softplus,
+                                      retn_dtype dtype, void* workspace, size_t workspace_bytes,
+                                      void* stream);
 
 /*
  * Backward of selective_scan_fwd for grad_y [B, N, D] and, optionally, grad_state_out

@@ -26,10 +26,12 @@ SIGNATURES = {
     "rotary_fwd": [_vp] * 6 + [_ll, _vp, _i, _ll] + [_i] * 7 + [_f, _f, _i, _vp],
     "rotary_bwd": [_vp] * 6 + [_ll, _vp, _i, _ll] + [_i] * 7 + [_f, _f, _i, _vp],
     "causal_conv_fwd": [_vp, _ll] + [_vp] * 6 + [_i] * 7 + [_vp],
+    "causal_conv_fwd_padded": [_vp, _ll] + [_vp] * 6 + [_i] * 7 + [_vp],
     "causal_conv_bwd": [_vp, _ll] + [_vp] * 10 + [_i] * 7 + [_vp, _sz, _vp],
     "causal_conv_bwd_workspace_bytes": [_i] * 5,
     "causal_conv_step": [_vp, _ll] + [_vp] * 4 + [_i] * 6 + [_vp],
     "selective_scan_fwd": [_vp] * 12 + [_ll] * 5 + [_i] * 7 + [_vp, _sz, _vp],
+    "selective_scan_fwd_padded": [_vp] * 12 + [_ll] * 5 + [_i] * 7 + [_vp, _sz, _vp],
     "selective_scan_workspace_bytes": [_i] * 5,
     "selective_scan_bwd": [_vp] * 21 + [_ll] * 5 + [_i] * 7 + [_vp, _sz, _vp],
     "selective_scan_bwd_workspace_bytes": [_i] * 5,
@@ -384,7 +386,8 @@ def causal_conv_fwd(x, weight, bias=None, silu=False, state_in=None, return_stat
     """Causal convolution of each channel of x [B,N,D] over its last K tokens with weight [D,K]
     (K 2, 3 or 4), plus bias [D], with an optional silu.  state_in / state_out [B,K-1,D]: the
     tokens in front of the first and the last K-1 tokens.  lengths [B] int32: tokens of each
-    sequence of a padded batch.  Returns y, or (y, state_out)."""
+    sequence of a padded batch; the rows of y behind them are zero, or, in a given `out`, left as
+    they were.  Returns y, or (y, state_out)."""
     torch = _torch()
     ldx, D, K, wcode = _conv_shapes(x, weight, bias, 3)
     B, N, dev, code = x.shape[0], x.shape[1], x.device, _code(x)
@@ -397,8 +400,9 @@ def causal_conv_fwd(x, weight, bias=None, silu=False, state_in=None, return_stat
         y = torch.empty((B, N, D), dtype=x.dtype, device=dev) if out is None else out
         if state_out is None and return_state:
             state_out = torch.empty((B, max(K - 1, 0), D), dtype=x.dtype, device=dev)
-        _check(_fn("causal_conv_fwd")(_ptr(x), ldx, _ptr(weight), _ptr(bias), _ptr(y), _ptr(state_in), _ptr(state_out),
-                                      _ptr(lengths), B, N, D, K, int(bool(silu)), code, wcode, s), "causal_conv_fwd")
+        fn = "causal_conv_fwd" if out is not None else "causal_conv_fwd_padded"     # fresh memory is written whole
+        _check(_fn(fn)(_ptr(x), ldx, _ptr(weight), _ptr(bias), _ptr(y), _ptr(state_in), _ptr(state_out), _ptr(lengths),
+                       B, N, D, K, int(bool(silu)), code, wcode, s), fn)
     return (y, state_out) if state_out is not None else y
 
 
@@ -485,7 +489,8 @@ def selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=
 
     x, dt, z [B,N,D] and Bm, Cm [B,N,G,S] (bf16 or fp32, token strides allowed); A [D,S], D and
     dt_bias [D], state_in and state_out [B,D,S] fp32 (state_out may be state_in); lengths [B] int32:
-    tokens of each sequence of a padded batch.  Returns y [B,N,D], or (y, state_out)."""
+    tokens of each sequence of a padded batch; the rows of y behind them are zero, or, in a given
+    `out`, left as they were.  Returns y [B,N,D], or (y, state_out)."""
     torch = _torch()
     ld, G, S, code = _scan_shapes(x, dt, A, Bm, Cm, D, z, dt_bias, False)
     (B, N, ch), dev = x.shape, x.device
@@ -499,10 +504,10 @@ def selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus=
         if state_out is None and return_state:
             state_out = torch.empty((B, ch, S), dtype=torch.float32, device=dev)
         ws, nbytes = _space(scan_workspace_bytes(B, N, ch, G, S), workspace, dev)
-        _check(_fn("selective_scan_fwd")(_ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
-                                         _ptr(dt_bias), _ptr(y), _ptr(state_in), _ptr(state_out), _ptr(lengths), *ld,
-                                         B, N, ch, G, S, int(bool(softplus)), code, _ptr(ws), nbytes, s),
-               "selective_scan_fwd")
+        fn = "selective_scan_fwd" if out is not None else "selective_scan_fwd_padded"     # fresh memory is written whole
+        _check(_fn(fn)(_ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(y),
+                       _ptr(state_in), _ptr(state_out), _ptr(lengths), *ld, B, N, ch, G, S, int(bool(softplus)), code,
+                       _ptr(ws), nbytes, s), fn)
     return (y, state_out) if state_out is not None else y
 
 

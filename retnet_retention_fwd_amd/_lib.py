@@ -49,10 +49,12 @@ EXPORTED = (
     "rotary_fwd",
     "rotary_bwd",
     "causal_conv_fwd",
+    "causal_conv_fwd_padded",
     "causal_conv_bwd",
     "causal_conv_bwd_workspace_bytes",
     "causal_conv_step",
     "selective_scan_fwd",
+    "selective_scan_fwd_padded",
     "selective_scan_workspace_bytes",
     "selective_scan_bwd",
     "selective_scan_bwd_workspace_bytes",

@@ -81,6 +81,7 @@ struct ConvArgs {
     void* gb;                  // backward, may be null
     int B, N, D, K;
     bool silu, bf16, w_bf16;
+    bool zero_behind;          // forward: the rows of y behind a length are zeros, else left as they were
     bool stream;               // set by the launchers
     float* workspace;
 };
@@ -105,6 +106,7 @@ struct ScanArgs {
     float *gA, *gD, *gbias, *gstate_in;            // gD, gbias, gstate_in may be null
     int B, N, D, G, S;
     bool softplus, bf16;
+    bool zero_behind;                              // forward, as ConvArgs'
     bool stream;                                   // set by the launchers
     float* workspace;
 };

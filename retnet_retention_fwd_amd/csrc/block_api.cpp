@@ -200,6 +200,100 @@ retn_status rotary_common(const void* q, const void* k, void* out_q, void* out_k
     return done(retn::launch_rotary(a, static_cast<hipStream_t>(stream)));
 }
 
+// The forward of the convolution and the scan; zero_behind: the rows of y behind a length are written as zeros.
+retn_status conv_forward(const void* x, long long ldx, const void* weight, const void* bias, void* y,
+                         const void* state_in, void* state_out, const int* lengths, int B, int N, int D, int K, int silu,
+                         retn_dtype dtype, retn_dtype wdtype, void* stream, bool zero_behind) {
+    if (!valid_types(dtype, wdtype)) return RETN_ERR_DTYPE;
+    const retn_status st = conv_sizes(B, N, D, K);
+    if (st != RETN_OK) return st;
+    if (ldx < D) return RETN_ERR_SHAPE;
+    if (ldx >= kMaxRow) return RETN_ERR_UNSUPPORTED;
+    const size_t tokens = sz(B) * N, es = elem_bytes(dtype), we = elem_bytes(wdtype), sb = sz(B) * (K - 1) * D * es;
+    if (B == 0) return RETN_OK;
+    if ((N > 0 && (x == nullptr || y == nullptr)) || weight == nullptr) return RETN_ERR_NULL;
+    const Range in[] = {opt(x, rows_bytes(tokens, ldx, D, es)), span(weight, sz(D) * K * we), opt(bias, D * we),
+                        opt(state_in, sb), opt(lengths, sizeof(int) * sz(B))};
+    const Range out[] = {opt(y, tokens * D * es), opt(state_out, sb)};
+    if (clash(in, out)) return RETN_ERR_ALIAS;
+    if (N == 0 && state_out == nullptr) return RETN_OK;
+    retn::ConvArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.w = weight;
+    a.b = bias;
+    a.lengths = lengths;
+    a.state_in = state_in;
+    a.state_out = state_out;
+    a.y = y;
+    a.B = B;
+    a.N = N;
+    a.D = D;
+    a.K = K;
+    a.silu = silu != 0;
+    a.zero_behind = zero_behind && lengths != nullptr;
+    a.bf16 = dtype == RETN_BF16;
+    a.w_bf16 = wdtype == RETN_BF16;
+    return done(retn::launch_conv_fwd(a, static_cast<hipStream_t>(stream)));
+}
+
+retn_status scan_forward(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                         const float* Dskip, const void* z, const float* dt_bias, void* y, const float* state_in,
+                         float* state_out, const int* lengths, long long ldx, long long lddt, long long ldz,
+                         long long ldb, long long ldc, int B, int N, int D, int G, int S, int softplus,
+                         retn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream, bool zero_behind) {
+    if (!valid_dtype(dtype)) return RETN_ERR_DTYPE;
+    const retn_status st = scan_sizes(B, N, D, G, S);
+    if (st != RETN_OK) return st;
+    const long long gs = static_cast<long long>(G) * S;
+    if (ldx < D || lddt < D || (z != nullptr && ldz < D) || ldb < gs || ldc < gs) return RETN_ERR_SHAPE;
+    if (far_rows(ldx, lddt, z != nullptr ? ldz : 0, ldb, ldc)) return RETN_ERR_UNSUPPORTED;
+    if (B == 0) return RETN_OK;
+    const size_t tokens = sz(B) * N, es = elem_bytes(dtype), ss = f32(sz(B) * D * S);
+    if (N > 0 && (x == nullptr || dt == nullptr || A == nullptr || Bm == nullptr || Cm == nullptr || y == nullptr))
+        return RETN_ERR_NULL;
+    const size_t need = selective_scan_workspace_bytes(B, N, D, G, S);
+    const bool in_place = state_out != nullptr && state_out == state_in;
+    const Range in[] = {opt(x, rows_bytes(tokens, ldx, D, es)), opt(dt, rows_bytes(tokens, lddt, D, es)),
+                        opt(A, f32(sz(D) * S)), opt(Bm, rows_bytes(tokens, ldb, gs, es)),
+                        opt(Cm, rows_bytes(tokens, ldc, gs, es)), opt(Dskip, f32(D)), opt(dt_bias, f32(D)),
+                        opt(z, rows_bytes(tokens, ldz, D, es)), opt(in_place ? nullptr : state_in, ss),
+                        opt(lengths, sizeof(int) * sz(B))};
+    const Range out[] = {opt(y, tokens * D * es), opt(state_out, ss), opt(workspace, need)};
+    if (clash(in, out)) return RETN_ERR_ALIAS;
+    if (bad_workspace(workspace, workspace_bytes, need)) return RETN_ERR_WORKSPACE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (N == 0) return done(retn::launch_copy_state(state_in, state_out, sz(B) * D * S, s));
+    retn::ScanArgs a{};
+    a.x = x;
+    a.dt = dt;
+    a.z = z;
+    a.Bm = Bm;
+    a.Cm = Cm;
+    a.ldx = ldx;
+    a.lddt = lddt;
+    a.ldz = ldz;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.A = A;
+    a.Dskip = Dskip;
+    a.bias = dt_bias;
+    a.lengths = lengths;
+    a.state_in = state_in;
+    a.state_out = state_out;
+    a.y = y;
+    a.B = B;
+    a.N = N;
+    a.D = D;
+    a.G = G;
+    a.S = S;
+    a.softplus = softplus != 0;
+    a.zero_behind = zero_behind && lengths != nullptr;
+    a.bf16 = dtype == RETN_BF16;
+    a.workspace = static_cast<float*>(workspace);
+    return done(retn::launch_scan_fwd(a, retn::scan_fwd_plan(B, N, D, G, S), s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -297,39 +391,16 @@ retn_status rotary_bwd(const void* grad_q, const void* grad_k, void* out_q, void
                          Hq, Hk, N, d, rot, interleaved, q_scale, k_scale, dtype, stream, true);
 }
 
-retn_status causal_conv_fwd(const void* x, long long ldx, const void* weight, const void* bias, void* y,
-                            const void* state_in, void* state_out, const int* lengths, int B, int N, int D, int K, int silu,
-                            retn_dtype dtype, retn_dtype wdtype, void* stream) {
-    if (!valid_types(dtype, wdtype)) return RETN_ERR_DTYPE;
-    const retn_status st = conv_sizes(B, N, D, K);
-    if (st != RETN_OK) return st;
-    if (ldx < D) return RETN_ERR_SHAPE;
-    if (ldx >= kMaxRow) return RETN_ERR_UNSUPPORTED;
-    const size_t tokens = sz(B) * N, es = elem_bytes(dtype), we = elem_bytes(wdtype), sb = sz(B) * (K - 1) * D * es;
-    if (B == 0) return RETN_OK;
-    if ((N > 0 && (x == nullptr || y == nullptr)) || weight == nullptr) return RETN_ERR_NULL;
-    const Range in[] = {opt(x, rows_bytes(tokens, ldx, D, es)), span(weight, sz(D) * K * we), opt(bias, D * we),
-                        opt(state_in, sb), opt(lengths, sizeof(int) * sz(B))};
-    const Range out[] = {opt(y, tokens * D * es), opt(state_out, sb)};
-    if (clash(in, out)) return RETN_ERR_ALIAS;
-    if (N == 0 && state_out == nullptr) return RETN_OK;
-    retn::ConvArgs a{};
-    a.x = x;
-    a.ldx = ldx;
-    a.w = weight;
-    a.b = bias;
-    a.lengths = lengths;
-    a.state_in = state_in;
-    a.state_out = state_out;
-    a.y = y;
-    a.B = B;
-    a.N = N;
-    a.D = D;
-    a.K = K;
-    a.silu = silu != 0;
-    a.bf16 = dtype == RETN_BF16;
-    a.w_bf16 = wdtype == RETN_BF16;
-    return done(retn::launch_conv_fwd(a, static_cast<hipStream_t>(stream)));
+retn_status causal_conv_fwd(const void* x, long long ldx, const void* weight, const void* bias,
+                            void* y, const void* state_in, void* state_out, const int* lengths, int B, int N, int D, int K,
+                            int silu, retn_dtype dtype, retn_dtype wdtype, void* stream) {
+    return conv_forward(x, ldx, weight, bias, y, state_in, state_out, lengths, B, N, D, K, silu, dtype, wdtype, stream, false);
+}
+
+retn_status causal_conv_fwd_padded(const void* x, long long ldx, const void* weight, const void* bias,
+                                   void* y, const void* state_in, void* state_out, const int* lengths, int B, int N, int D,
+                                   int K, int silu, retn_dtype dtype, retn_dtype wdtype, void* stream) {
+    return conv_forward(x, ldx, weight, bias, y, state_in, state_out, lengths, B, N, D, K, silu, dtype, wdtype, stream, true);
 }
 
 size_t causal_conv_bwd_workspace_bytes(int B, int N, int D, int K, retn_dtype dtype) {
@@ -425,55 +496,17 @@ retn_status selective_scan_fwd(const void* x, const void* dt, const float* A, co
                                float* state_out, const int* lengths, long long ldx, long long lddt, long long ldz,
                                long long ldb, long long ldc, int B, int N, int D, int G, int S, int softplus,
                                retn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
-    if (!valid_dtype(dtype)) return RETN_ERR_DTYPE;
-    const retn_status st = scan_sizes(B, N, D, G, S);
-    if (st != RETN_OK) return st;
-    const long long gs = static_cast<long long>(G) * S;
-    if (ldx < D || lddt < D || (z != nullptr && ldz < D) || ldb < gs || ldc < gs) return RETN_ERR_SHAPE;
-    if (far_rows(ldx, lddt, z != nullptr ? ldz : 0, ldb, ldc)) return RETN_ERR_UNSUPPORTED;
-    if (B == 0) return RETN_OK;
-    const size_t tokens = sz(B) * N, es = elem_bytes(dtype), ss = f32(sz(B) * D * S);
-    if (N > 0 && (x == nullptr || dt == nullptr || A == nullptr || Bm == nullptr || Cm == nullptr || y == nullptr))
-        return RETN_ERR_NULL;
-    const size_t need = selective_scan_workspace_bytes(B, N, D, G, S);
-    const bool in_place = state_out != nullptr && state_out == state_in;
-    const Range in[] = {opt(x, rows_bytes(tokens, ldx, D, es)), opt(dt, rows_bytes(tokens, lddt, D, es)),
-                        opt(A, f32(sz(D) * S)), opt(Bm, rows_bytes(tokens, ldb, gs, es)),
-                        opt(Cm, rows_bytes(tokens, ldc, gs, es)), opt(Dskip, f32(D)), opt(dt_bias, f32(D)),
-                        opt(z, rows_bytes(tokens, ldz, D, es)), opt(in_place ? nullptr : state_in, ss),
-                        opt(lengths, sizeof(int) * sz(B))};
-    const Range out[] = {opt(y, tokens * D * es), opt(state_out, ss), opt(workspace, need)};
-    if (clash(in, out)) return RETN_ERR_ALIAS;
-    if (bad_workspace(workspace, workspace_bytes, need)) return RETN_ERR_WORKSPACE;
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    if (N == 0) return done(retn::launch_copy_state(state_in, state_out, sz(B) * D * S, s));
-    retn::ScanArgs a{};
-    a.x = x;
-    a.dt = dt;
-    a.z = z;
-    a.Bm = Bm;
-    a.Cm = Cm;
-    a.ldx = ldx;
-    a.lddt = lddt;
-    a.ldz = ldz;
-    a.ldb = ldb;
-    a.ldc = ldc;
-    a.A = A;
-    a.Dskip = Dskip;
-    a.bias = dt_bias;
-    a.lengths = lengths;
-    a.state_in = state_in;
-    a.state_out = state_out;
-    a.y = y;
-    a.B = B;
-    a.N = N;
-    a.D = D;
-    a.G = G;
-    a.S = S;
-    a.softplus = softplus != 0;
-    a.bf16 = dtype == RETN_BF16;
-    a.workspace = static_cast<float*>(workspace);
-    return done(retn::launch_scan_fwd(a, retn::scan_fwd_plan(B, N, D, G, S), s));
+    return scan_forward(x, dt, A, Bm, Cm, Dskip, z, dt_bias, y, state_in, state_out, lengths, ldx, lddt, ldz, ldb, ldc, B, N,
+                        D, G, S, softplus, dtype, workspace, workspace_bytes, stream, false);
+}
+
+retn_status selective_scan_fwd_padded(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                                      const float* Dskip, const void* z, const float* dt_bias, void* y, const float* state_in,
+                                      float* state_out, const int* lengths, long long ldx, long long lddt, long long ldz,
+                                      long long ldb, long long ldc, int B, int N, int D, int G, int S, int softplus,
+                                      retn_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    return scan_forward(x, dt, A, Bm, Cm, Dskip, z, dt_bias, y, state_in, state_out, lengths, ldx, lddt, ldz, ldb, ldc, B, N,
+                        D, G, S, softplus, dtype, workspace, workspace_bytes, stream, true);
 }
 
 size_t selective_scan_bwd_workspace_bytes(int B, int N, int D, int G, int S) {

@@ -78,6 +78,13 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, int pack
     if (b >= a.B) return;
     const int n = length_of(a.lengths, b, a.N), t0 = tile * walk, left = a.D - c;
     const bool last = tile == (n > 0 ? (n - 1) / walk : 0);
+    if (a.zero_behind) {
+        // this walk's rows behind the sequence's last token
+        const int end = t0 + walk < a.N ? t0 + walk : a.N;
+        const float zero[V] = {};
+        for (int t = t0 > n ? t0 : n; t < end; ++t)
+            put<T, WHOLE>(static_cast<T*>(a.y) + (static_cast<size_t>(b) * a.N + t) * a.D + c, zero, left, false);
+    }
     if (t0 < n) {
         const int end = t0 + walk < n ? t0 + walk : n;
         const T* x = static_cast<const T*>(a.x) + static_cast<size_t>(b) * a.N * a.ldx + c;

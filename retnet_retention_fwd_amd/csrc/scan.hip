@@ -63,6 +63,11 @@ __global__ __launch_bounds__(kScanThreads, SP <= 16 ? 4 : 2) void scan_fwd_kerne
     T* yp = static_cast<T*>(a.y) + tok0 * a.D;
     const uint32_t at = static_cast<uint32_t>(ch) * sizeof(T);
     const bool gated = !STATE && a.z != nullptr;
+    if (!STATE && a.zero_behind && on) {
+        // this segment's rows behind the sequence's last token
+        for (int t = p.t_begin > p.t_end ? p.t_begin : p.t_end; t < p.t_full; ++t)
+            row_put(yp + static_cast<size_t>(t) * a.D, at, T(0));
+    }
 
     // one token's step of all states; its read-out
     auto step = [&](float dt, float x, float B, auto tok, const Read& C) __attribute__((always_inline)) {

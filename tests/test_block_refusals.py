@@ -1,0 +1,37 @@
+"""More refusals of the operators around the retention (no GPU: every call here fails validation
+and returns before anything is enqueued)."""
+import pytest
+
+pytest.importorskip("torch")
+
+from retnet_retention_fwd_amd import _block  # noqa: E402
+from test_block_abi import (BF16, ERR_ALIAS, ERR_DTYPE, ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED, ERR_WORKSPACE, F32, MB,  # noqa: E402
+                            OK, SCAN_IN, SCAN_LD, at, call)
+
+
+def conv_padded(**kw):
+    return call("causal_conv_fwd_padded", dict(x=at(0), ldx=64, w=at(1), b=at(2), y=at(3), si=at(4), so=at(5), n=at(6), B=2,
+                                               N=8, D=64, K=4, silu=1, dt=BF16, wt=BF16, stream=None), **kw)
+
+
+def scan_padded(**kw):
+    return call("selective_scan_fwd_padded", dict(**SCAN_IN, y=at(8), si=at(9), so=at(10), n=at(11), **SCAN_LD, B=2, N=8,
+                                                  ch=64, G=1, S=16, sp=1, dtype=BF16, ws=at(12), wsb=64 * MB, stream=None),
+                **kw)
+
+
+def test_padded_forms():
+    """They check what the forms beside them check."""
+    c, s = conv_padded, scan_padded
+    assert c(dt=9) == ERR_DTYPE and c(dt=F32, wt=BF16) == ERR_DTYPE and s(dtype=9) == ERR_DTYPE
+    assert c(B=-1) == ERR_SHAPE and c(ldx=63) == ERR_SHAPE and s(S=0) == ERR_SHAPE and s(ldb=15) == ERR_SHAPE
+    assert c(K=5) == ERR_UNSUPPORTED and s(S=65, ldb=65, ldc=65) == ERR_UNSUPPORTED
+    assert c(x=None) == ERR_NULL and c(y=None) == ERR_NULL and s(A=None) == ERR_NULL and s(y=None) == ERR_NULL
+    assert c(y=at(0)) == ERR_ALIAS and c(y=at(6)) == ERR_ALIAS and s(y=at(6)) == ERR_ALIAS and s(so=at(11)) == ERR_ALIAS
+    assert s(B=1, N=4096, ws=None) == ERR_WORKSPACE and s(B=1, N=4096, ws=at(12) + 4) == ERR_WORKSPACE
+    assert c(B=0) == OK and c(N=0, so=None) == OK and s(B=0) == OK and s(N=0, so=None) == OK
+
+
+def test_padded_forms_take_the_same_arguments():
+    for n in ("causal_conv_fwd", "selective_scan_fwd"):
+        assert _block.SIGNATURES[n] == _block.SIGNATURES[n + "_padded"]
