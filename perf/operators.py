@@ -348,7 +348,7 @@ def _own(s):
     if op == "conv":
         if way == "fwd":
             return R.causal_conv_fwd(s["x"], s["w"], s["b"], silu=s["silu"], state_in=s["state"], return_state=True,
-                                     lengths=s["lengths"], out=s["y"])
+                                     lengths=s["lengths"])      # which writes the rows behind the ends as zeros
         if way == "step":
             return R.causal_conv_step(s["x"], s["w"], s["state"], s["b"], silu=s["silu"]), s["state"]
         return R.causal_conv_bwd(s["x"], s["w"], s["gy"], s["b"], silu=s["silu"], state_in=s["state"],
@@ -356,7 +356,7 @@ def _own(s):
     if way == "fwd":
         return R.selective_scan_fwd(s["x"], s["dt"], s["A"], s["Bm"], s["Cm"], D=s["Dskip"], z=s["z"],
                                     dt_bias=s["bias"], softplus=True, state_in=s["state"], return_state=True,
-                                    lengths=s["lengths"], out=s["y"])
+                                    lengths=s["lengths"])
     if way == "step":
         return R.selective_scan_step(s["x"], s["dt"], s["A"], s["Bm"], s["Cm"], s["state"], D=s["Dskip"], z=s["z"],
                                      dt_bias=s["bias"], softplus=True), s["state"]
