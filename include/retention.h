@@ -395,7 +395,8 @@ retn_status rotary_table(float* table, const double* freq, int pairs, long long 
  *   table      [table_len, rot/2, 2] fp32
  *   positions  optional int64, device memory: [N], or [B, N] if positions_per_batch; NULL:
  *              token n has position first + n (0 <= first, first + N <= table_len).  A
- *              position outside 0 .. table_len - 1 turns its row's rotated part into NaN.
+ *              position outside 0 .. table_len - 1 turns its row's rotated part into NaN
+ *              (table_len >= 1).
  *   d <= 256, rot even, 2 <= rot <= d
  */
 retn_status rotary_fwd(const void* q, const void* k, void* out_q, void* out_k,

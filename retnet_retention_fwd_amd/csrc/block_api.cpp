@@ -159,7 +159,8 @@ retn_status rotary_common(const void* q, const void* k, void* out_q, void* out_k
     if ((Hq > 0 && (q == nullptr || out_q == nullptr)) || (Hk > 0 && (k == nullptr || out_k == nullptr)) ||
         strides == nullptr || table == nullptr)
         return RETN_ERR_NULL;
-    if (positions == nullptr && (first < 0 || first > table_len - N)) return RETN_ERR_SHAPE;
+    // (the kernel reads row 0 for a position outside of the table)
+    if (positions == nullptr ? first < 0 || first > table_len - N : table_len < 1) return RETN_ERR_SHAPE;
     const View v[4] = {{strides[0], strides[1], strides[2]}, {strides[3], strides[4], strides[5]},
                        {strides[6], strides[7], strides[8]}, {strides[9], strides[10], strides[11]}};
     const int H[4] = {Hq, Hq, Hk, Hk};

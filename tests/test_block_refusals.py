@@ -6,7 +6,7 @@ pytest.importorskip("torch")
 
 from retnet_retention_fwd_amd import _block  # noqa: E402
 from test_block_abi import (BF16, ERR_ALIAS, ERR_DTYPE, ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED, ERR_WORKSPACE, F32, MB,  # noqa: E402
-                            OK, SCAN_IN, SCAN_LD, at, call)
+                            OK, SCAN_IN, SCAN_LD, at, call, rotary)
 
 
 def conv_padded(**kw):
@@ -35,3 +35,12 @@ def test_padded_forms():
 def test_padded_forms_take_the_same_arguments():
     for n in ("causal_conv_fwd", "selective_scan_fwd"):
         assert _block.SIGNATURES[n] == _block.SIGNATURES[n + "_padded"]
+
+
+@pytest.mark.parametrize("name", ["rotary_fwd", "rotary_bwd"])
+def test_positions_need_a_table(name):
+    """An unknown position turns its row into NaN, but a table without rows has no row to read."""
+    assert rotary(name, length=0, pos=at(5)) == ERR_SHAPE
+    assert rotary(name, length=0, pos=at(5), batched=1) == ERR_SHAPE
+    assert rotary(name, length=0) == ERR_SHAPE
+    assert rotary(name, length=0, pos=at(5), N=0) == OK
