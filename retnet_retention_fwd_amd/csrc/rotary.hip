@@ -23,16 +23,17 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kInFlight = 4;               // heads whose loads are issued together
 constexpr size_t kWantThreads = 1 << 17;   // 8 waves of 64 for each of 256 CUs
+constexpr size_t kMostGroups = 1 << 23;    // of one launch, which takes 2^32 threads at most
 
 // V elements a side: interleaved, V adjacent elements (V / 2 pairs); halves, V pairs with
 // one pack in each half.  V = 0: one pair a thread, any sizes.
 template <typename T, bool INTER, int V>
-__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, int units, int heads_per) {
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a, size_t tok0, int units, int heads_per) {
     constexpr int E = V > 0 ? V : (INTER ? 2 : 1);   // adjacent elements of a pack
     constexpr int PAIRS = INTER ? E / 2 : E;
     const int tpb = kThreads / units;                // tokens of a workgroup
     const int u = threadIdx.x % units;
-    const size_t tok = static_cast<size_t>(blockIdx.x) * tpb + threadIdx.x / units;
+    const size_t tok = tok0 + static_cast<size_t>(blockIdx.x) * tpb + threadIdx.x / units;
     if (threadIdx.x >= tpb * units || tok >= static_cast<size_t>(a.B) * a.N) return;
     const int b = static_cast<int>(tok / a.N), n = static_cast<int>(tok % a.N);
     // a unit rotates, or copies elements behind the rotated part
@@ -136,13 +137,20 @@ hipError_t launch_typed(const RotaryArgs& a, hipStream_t st) {
     int per = 16;
     while (per > 1 && tokens * units * ((heads + per - 1) / per) < kWantThreads) per /= 2;
     const int tpb = kThreads / units;
-    const dim3 grid(static_cast<unsigned>((tokens + tpb - 1) / tpb), (heads + per - 1) / per), block(kThreads);
+    const size_t groups = (tokens + tpb - 1) / tpb;
     ProfScope prof(kProfRotary, st);
-    if (packs)
-        hipLaunchKernelGGL((rotary_kernel<T, INTER, V>), grid, block, 0, st, a, units, per);
-    else
-        hipLaunchKernelGGL((rotary_kernel<T, INTER, 0>), grid, block, 0, st, a, units, per);
-    return hipGetLastError();
+    // (one launch, unless there are more than 8M workgroups: heads without packs, a token each)
+    for (size_t g = 0; g < groups; g += kMostGroups) {
+        const size_t now = groups - g < kMostGroups ? groups - g : kMostGroups;
+        const dim3 grid(static_cast<unsigned>(now), (heads + per - 1) / per), block(kThreads);
+        if (packs)
+            hipLaunchKernelGGL((rotary_kernel<T, INTER, V>), grid, block, 0, st, a, g * tpb, units, per);
+        else
+            hipLaunchKernelGGL((rotary_kernel<T, INTER, 0>), grid, block, 0, st, a, g * tpb, units, per);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
