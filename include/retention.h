@@ -341,8 +341,10 @@ double retention_calib_mfma_flops(int blocks, int waves, int iters);
  *              as zeros), gradient rows there are zero, and a final state is the one behind
  *              the last of those tokens.
  *   Limits     D <= 2^20, B * N <= 2^31 - 2^16, B * D < 2^31, B * N * D < 2^34 (rotary:
- *              B * N * d < 2^32, Hq + Hk < 2^16), row strides < 2^26; else
- *              RETN_ERR_UNSUPPORTED.
+ *              B * N * d < 2^32, Hq + Hk < 2^16; its table: 2^32 - 2^8 pairs, 2^31 rows;
+ *              convolution's gradient: B * ceil(N / 128) * (D / 32 + 1) < 2^23; scan:
+ *              B * N * G * S <= 2^31 - 2^7, B * (D / 16 + G) < 2^23), row strides < 2^26;
+ *              else RETN_ERR_UNSUPPORTED.
  * All results are the same from call to call (no atomics).
  */
 

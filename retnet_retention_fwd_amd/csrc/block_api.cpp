@@ -21,6 +21,7 @@ constexpr int kMaxStates = 64;
 constexpr int kMaxHead = 256;
 constexpr unsigned long long kMaxElements = 1ull << 34;   // of a [B, N, D] tensor
 constexpr unsigned long long kMaxGroups = 1ull << 23;     // workgroups of a launch (2^32 threads at most)
+constexpr unsigned long long kMaxLaunch = (1ull << 32) - 256;   // elements of a launch of one a thread, in whole workgroups
 constexpr long long kMaxRow = 1ll << 26;                  // elements from one token to the next
 constexpr long long kMaxSpan = 1ll << 40;                 // elements that one axis of a view spans
 constexpr size_t kMaxTokens = (1ull << 31) - (1 << 16);   // token numbers and steps ahead of them are ints
@@ -82,8 +83,9 @@ retn_status scan_sizes(int B, int N, int D, int G, int S) {
     const retn_status st = seq_sizes(B, N, D);
     if (st != RETN_OK) return st;
     if (D % G != 0) return RETN_ERR_SHAPE;
-    // one workgroup a (sequence, block of 16 channels or more), cut into 1024 segments at most
-    if (S > kMaxStates || sz(B) * (sz(D) / 16 + G) >= kMaxGroups || sz(B) * N * G * S >= (1ull << 31))
+    // one workgroup a (sequence, block of 16 channels or more); the gradients of B and C one element a
+    // thread.  (What is cut into segments has fewer than 2048 waves uncut, fewer than 6144 cut.)
+    if (S > kMaxStates || sz(B) * (sz(D) / 16 + G) >= kMaxGroups || 2 * sz(B) * N * G * S > kMaxLaunch)
         return RETN_ERR_UNSUPPORTED;
     return RETN_OK;
 }
@@ -367,8 +369,7 @@ retn_status layer_norm_bwd(const void* x, const void* weight, const float* mean,
 retn_status rotary_table(float* table, const double* freq, int pairs, long long first, long long count, float magnitude,
                          void* stream) {
     if (pairs < 1 || count < 0 || first < 0) return RETN_ERR_SHAPE;
-    if (pairs > kMaxHead / 2 || static_cast<unsigned long long>(count) * pairs >= (1ull << 32) ||
-        static_cast<unsigned long long>(count) > (1ull << 31) || first > (1ll << 40))
+    if (pairs > kMaxHead / 2 || count > (1ll << 31) || sz(count) * pairs > kMaxLaunch || first > (1ll << 40))
         return RETN_ERR_UNSUPPORTED;
     if (count == 0) return RETN_OK;
     if (table == nullptr || freq == nullptr) return RETN_ERR_NULL;

@@ -6,7 +6,7 @@ pytest.importorskip("torch")
 
 from retnet_retention_fwd_amd import _block  # noqa: E402
 from test_block_abi import (BF16, ERR_ALIAS, ERR_DTYPE, ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED, ERR_WORKSPACE, F32, MB,  # noqa: E402
-                            OK, SCAN_IN, SCAN_LD, at, call, rotary)
+                            OK, SCAN_IN, SCAN_LD, at, call, rotary, scan_bwd)
 
 
 def conv_padded(**kw):
@@ -44,3 +44,14 @@ def test_positions_need_a_table(name):
     assert rotary(name, length=0, pos=at(5), batched=1) == ERR_SHAPE
     assert rotary(name, length=0) == ERR_SHAPE
     assert rotary(name, length=0, pos=at(5), N=0) == OK
+
+
+def test_launches_of_whole_workgroups():
+    """Element counts whose last, partly idle workgroup would bring a launch to 2^32 threads."""
+    table = lambda **kw: call("rotary_table", dict(t=at(0), f=1 << 39, pairs=2, first=0, n=10, m=1.0, s=None), **kw)  # noqa: E731
+    assert table(n=(1 << 31) - 1) == ERR_UNSUPPORTED
+    # 2 B N G S elements of the gradients of B and C, one a thread
+    for f in (scan_padded, scan_bwd):
+        assert f(B=1, N=(1 << 30) - 1, ch=2, G=1, S=2, ldx=2, lddt=2, ldz=2, ldb=2, ldc=2) == ERR_UNSUPPORTED
+    assert _block.scan_bwd_workspace_bytes(1, (1 << 30) - 1, 2, 1, 2) == 0
+    assert _block.scan_bwd_workspace_bytes(1, (1 << 30) - 64, 2, 1, 2) > 0
