@@ -199,6 +199,15 @@ __device__ __forceinline__ void store_state(float* p, int S, const float (&h)[SP
         if (i < S) raw_store_n<float, 4>(p + i, Raw<float, 4>{{h[i], h[i + 1], h[i + 2], h[i + 3]}}, S - i);
 }
 
+// A state carried over tokens of log2 decay x in all: 2^x e + own.  Where tokens grow (A dt > 0) the
+// factor of many can overflow although none of theirs does: it is then applied in two halves, and
+// a state of zero stays zero, as token by token.
+__device__ __forceinline__ float carry(float x, float e, float own) {
+    const bool far = x > 127.f;
+    const float f = exp2_fast(far ? 0.5f * x : x);
+    return e != 0.f ? fmaf(f, far ? f * e : e, own) : own;
+}
+
 // Entry states of a sequence's segments.  Along the walk (from the last segment to the first
 // with BACK) segment k takes e_k in and leaves e_(k+1) = exp(A sum_k dt) e_k + own_k, own_k
 // being what it makes of a zero state: `at` holds own and gets e.  A lane takes a (channel,
@@ -239,14 +248,14 @@ __device__ __forceinline__ void compose(float* at, const float* sum, size_t ds, 
             fetch(k);
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                h = fmaf(exp2_fast(A2 * dt[i]), h, own[i]);
+                h = carry(A2 * dt[i], h, own[i]);
                 total += dt[i];
             }
         }
         sums.own[wave][lane] = h;
         sums.dt[wave][lane] = total;
         __syncthreads();
-        for (int w = 0; w < wave; ++w) e = fmaf(exp2_fast(A2 * sums.dt[w][lane]), e, sums.own[w][lane]);
+        for (int w = 0; w < wave; ++w) e = carry(A2 * sums.dt[w][lane], e, sums.own[w][lane]);
     }
     for (int k = k0; k < k1; k += U) {
         fetch(k);
@@ -254,7 +263,7 @@ __device__ __forceinline__ void compose(float* at, const float* sum, size_t ds, 
         for (int i = 0; i < U; ++i) {
             if (k + i >= k1) break;
             at[(BACK ? nseg - 1 - k - i : k + i) * ds] = e;
-            e = fmaf(exp2_fast(A2 * dt[i]), e, own[i]);
+            e = carry(A2 * dt[i], e, own[i]);
         }
     }
 }

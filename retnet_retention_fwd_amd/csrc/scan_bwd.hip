@@ -479,7 +479,7 @@ __global__ __launch_bounds__(kScanThreads, LPC == 16 || (LPC == 4 && sizeof(T) =
             float e[SPL];
             load_lane(entry, e);
 #pragma unroll
-            for (int i = 0; i < SPL; ++i) h0[i] = fmaf(exp2_fast(cum * A2[i]), e[i], h0[i]);
+            for (int i = 0; i < SPL; ++i) h0[i] = carry(cum * A2[i], e[i], h0[i]);
         }
         const Pack k = pack();
         if (k.ur < kTile) {
