@@ -138,6 +138,8 @@ def _rows(t, name, dtype, dev, shape, inner=1):
     size, step = t.shape, t.stride()
     if shape is not None and size != shape:
         _shape(t, name, shape)
+    if len(size) <= inner:
+        raise ValueError(f"{name} must be [B,N,...] or [B,...], got {list(size)}")
     width = 1
     for i in range(1, inner + 1):
         if step[-i] != width and size[-i] != 1:
@@ -163,6 +165,8 @@ def _weights(w, b, x, w_shape, D):
     first = w if w is not None else b
     if first is None:
         return RETN_F32
+    if not isinstance(first, torch.Tensor):
+        raise TypeError(f"{'bias' if w is None else 'weight'} must be a torch.Tensor")
     if first.dtype not in (torch.float32, x.dtype):
         raise TypeError(f"weight and bias must be float32 or {x.dtype}, got {first.dtype}")
     _given(w, "weight", first.dtype, x.device, w_shape)
@@ -275,17 +279,26 @@ def rotary_frequencies(rot, base=10000.0, scaling="none", factor=1.0, original_l
     return freq
 
 
+def _table_device(at, device):
+    """The GPU of a table of frequencies at `at`: the one asked for, theirs, or the current one."""
+    torch = _torch()
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise ValueError(f"device must be a GPU, got {dev}")
+    if at.type == "cuda":
+        if dev.index not in (None, at.index):
+            raise ValueError(f"device is {dev}, freq is on {at}")
+        return at
+    return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
 def rotary_table(freq, count, first=0, magnitude=1.0, device=None, stream=None):
     """Table [count, rot/2, 2] fp32 of magnitude * (cos, sin) for positions first ..
     first + count - 1 and the angular frequencies freq [rot/2] (rotary_frequencies)."""
     torch = _torch()
     if not isinstance(freq, torch.Tensor) or freq.dim() != 1 or freq.dtype != torch.float64:
         raise TypeError("freq must be a float64 tensor [rot/2]")
-    dev = torch.device("cuda") if device is None else torch.device(device)
-    if freq.is_cuda:
-        dev = freq.device
-    elif dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
+    dev = _table_device(freq.device, device)
     on, s = _on(dev, stream)
     with on:
         f = freq.to(dev).contiguous()
@@ -314,6 +327,16 @@ def _heads(t, name, dtype, dev, shape):
     return step[:3]
 
 
+def _positions(positions, dev, B, N):
+    """Whether they are one row a sequence, and their address."""
+    torch = _torch()
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    batched = int(positions.dim() == 2)
+    _dense(positions, "positions", torch.int64, dev, (B, N) if batched else (N,))
+    return batched, positions.data_ptr()
+
+
 def _rotary(fn, q, k, table, positions, offset, interleaved, q_scale, k_scale, out_q, out_k, stream):
     torch = _torch()
     sq = _heads(q, "q", None, None, None)
@@ -330,10 +353,7 @@ def _rotary(fn, q, k, table, positions, offset, interleaved, q_scale, k_scale, o
         Hk, pk = k.shape[1], k.data_ptr()
         if k.shape != (B, Hk, N, d):
             raise ValueError(f"k must be [{B}, Hk, {N}, {d}], got {list(k.shape)}")
-    batched, pp = 0, None
-    if positions is not None:
-        batched, pp = int(positions.dim() == 2), positions.data_ptr()
-        _dense(positions, "positions", torch.int64, dev, (B, N) if batched else (N,))
+    batched, pp = (0, None) if positions is None else _positions(positions, dev, B, N)
     on, s = _on(dev, stream)
     with on:
         if out_q is None:
@@ -376,6 +396,8 @@ def _conv_shapes(x, weight, bias, dims):
     if x.dim() != dims:
         raise ValueError("x must be " + ("[B,N,D]" if dims == 3 else "[B,D]"))
     D = x.shape[-1]
+    if weight is not None and not isinstance(weight, _torch().Tensor):
+        raise TypeError("weight must be a torch.Tensor")
     if weight is None or weight.dim() != 2 or weight.shape[0] != D:
         raise ValueError(f"weight must be [{D}, K]")
     return ldx, D, weight.shape[1], _weights(weight, bias, x, weight.shape, D)

@@ -2,7 +2,7 @@
 and returns before anything is enqueued)."""
 import pytest
 
-pytest.importorskip("torch")
+torch = pytest.importorskip("torch")
 
 from retnet_retention_fwd_amd import _block  # noqa: E402
 from test_block_abi import (BF16, ERR_ALIAS, ERR_DTYPE, ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED, ERR_WORKSPACE, F32, MB,  # noqa: E402
@@ -55,3 +55,40 @@ def test_launches_of_whole_workgroups():
         assert f(B=1, N=(1 << 30) - 1, ch=2, G=1, S=2, ldx=2, lddt=2, ldz=2, ldb=2, ldc=2) == ERR_UNSUPPORTED
     assert _block.scan_bwd_workspace_bytes(1, (1 << 30) - 1, 2, 1, 2) == 0
     assert _block.scan_bwd_workspace_bytes(1, (1 << 30) - 64, 2, 1, 2) > 0
+
+
+class Seen(torch.Tensor):
+    """A tensor that only claims to be on the GPU."""
+    is_cuda = True
+
+
+def seen(*shape, dtype=None):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(Seen)
+
+
+def test_arguments_of_the_wrong_kind_are_named():
+    R = _block
+    x, w = seen(2, 3, 8), seen(8, 4)
+    for f in (lambda: R.causal_conv_fwd(seen(8), w), lambda: R.causal_conv_step(seen(8), w, seen(2, 3, 8)),
+              lambda: R.selective_scan_fwd(seen(8), x, seen(8, 4), x, x),
+              lambda: R.selective_scan_step(seen(8), x, seen(8, 4), x, seen(2, 8, 4), x)):
+        with pytest.raises(ValueError, match="x must be"):
+            f()
+    for f in (lambda: R.layer_norm_fwd(seen(2, 8), [1.0] * 8), lambda: R.causal_conv_fwd(x, [[1.0] * 4] * 8)):
+        with pytest.raises(TypeError, match="weight must be a torch.Tensor"):
+            f()
+    with pytest.raises(TypeError, match="bias must be a torch.Tensor"):
+        R.layer_norm_fwd(seen(2, 8), None, 1.0)
+    with pytest.raises(TypeError, match="positions must be a torch.Tensor"):
+        R._positions([0, 1, 2], None, 1, 3)
+
+
+def test_table_is_built_where_it_is_asked_for():
+    freq = _block.rotary_frequencies(8)
+    with pytest.raises(ValueError, match="device"):
+        _block.rotary_table(freq, 4, device="cpu")
+    with pytest.raises(ValueError, match="device"):
+        _block._table_device(torch.device("cuda", 0), "cuda:1")
+    assert _block._table_device(torch.device("cuda", 1), None) == torch.device("cuda", 1)
+    assert _block._table_device(torch.device("cuda", 1), "cuda") == torch.device("cuda", 1)
+    assert _block._table_device(torch.device("cpu"), "cuda:1") == torch.device("cuda", 1)
