@@ -173,8 +173,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_bwd_kernel(NormArgs a) {
         for (int i = 0; i < V; ++i) gw[p][i] = gb[p][i] = 0.f;
     }
     const float inv = 1.f / static_cast<float>(D);
-    // the next row is in flight while one is worked on, where registers allow it
-    constexpr bool AHEAD = F <= 16;
+    // the next row is in flight while one is worked on
     Raw<T, V> rx[P], rg[P];
     float mean = 0.f, rstd = 0.f;
     auto fetch = [&](size_t r) {
@@ -194,11 +193,10 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_bwd_kernel(NormArgs a) {
         rstd = there ? a.rstd[r] : 0.f;
     };
     const size_t stride = static_cast<size_t>(gridDim.x) * RPB;
-    if (AHEAD) fetch(static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / TPR);
+    fetch(static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / TPR);
     for (size_t r0 = static_cast<size_t>(blockIdx.x) * RPB; r0 < a.rows; r0 += stride) {
         const size_t r = r0 + threadIdx.x / TPR;
         const bool live = r < a.rows;
-        if (!AHEAD) fetch(r);
         const float scale = rstd;
         float xh[P][V], v[P][V], s = 0.f, sx = 0.f;
 #pragma unroll
@@ -214,7 +212,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_bwd_kernel(NormArgs a) {
                 sx = fmaf(v[p][i], xh[p][i], sx);
             }
         }
-        if (AHEAD && r0 + stride < a.rows) fetch(r + stride);
+        if (r0 + stride < a.rows) fetch(r + stride);
         row_sum2<TPR>(s, sx, red, slot);
         if (!live) continue;
         const float m1 = s * inv, m2 = sx * inv;
