@@ -230,7 +230,7 @@ __device__ __forceinline__ void compose(float* at, const float* sum, size_t ds, 
     const int lane = threadIdx.x & 63, wave = WAVES > 1 ? threadIdx.x >> 6 : 0;
     const int each = (nseg + WAVES - 1) / WAVES, k0 = wave * each;
     const int k1 = k0 + each < nseg ? k0 + each : nseg;
-    float own[U], dt[U];
+    float own[U], dt[U];                       // (dt: then its log2 decay)
     auto fetch = [&](int k) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -241,15 +241,26 @@ __device__ __forceinline__ void compose(float* at, const float* sum, size_t ds, 
             dt[i] = hands ? sum[static_cast<size_t>(s) * D] : 0.f;
         }
     };
+    // the fetched segments' factors; whether a lane of the wave has one beyond fp32
+    auto decays = [&]() {
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) most = fmaxf(most, dt[i] *= A2);
+        return __any(most > 127.f);
+    };
     float e = init;
     if constexpr (WAVES > 1) {
         float h = 0.f, total = 0.f;
         for (int k = k0; k < k1; k += U) {
             fetch(k);
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                h = carry(A2 * dt[i], h, own[i]);
-                total += dt[i];
+            for (int i = 0; i < U; ++i) total += dt[i];
+            if (decays()) {
+#pragma unroll
+                for (int i = 0; i < U; ++i) h = carry(dt[i], h, own[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < U; ++i) h = fmaf(exp2_fast(dt[i]), h, own[i]);
             }
         }
         sums.own[wave][lane] = h;
@@ -259,12 +270,18 @@ __device__ __forceinline__ void compose(float* at, const float* sum, size_t ds, 
     }
     for (int k = k0; k < k1; k += U) {
         fetch(k);
+        auto walk = [&](auto next) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (k + i >= k1) break;
-            at[(BACK ? nseg - 1 - k - i : k + i) * ds] = e;
-            e = carry(A2 * dt[i], e, own[i]);
-        }
+            for (int i = 0; i < U; ++i) {
+                if (k + i >= k1) break;
+                at[(BACK ? nseg - 1 - k - i : k + i) * ds] = e;
+                e = next(dt[i], e, own[i]);
+            }
+        };
+        if (decays())
+            walk(carry);
+        else
+            walk([](float x, float e, float own) { return fmaf(exp2_fast(x), e, own); });
     }
 }
 inline int compose_waves(int nseg, size_t pairs) { return nseg > 48 && pairs <= 32768 ? kComposeWaves : 1; }
