@@ -14,9 +14,12 @@
 // gradient needs, so it reads x and gy once too and keeps its channels' weight sums in
 // registers until the end of the walk.
 //
-// Measured, bf16: forward of 2 x 8191 x 2048 channels 23 us for 88 MB (3.8 TB/s; the sequences'
-// ragged ends leave rows out); backward of 4 x 2048 x 2048 31 us for 101 MB (3.3 TB/s, the
-// vector ALUs 56% busy with silu and its derivative).
+// Measured, bf16: forward of 2 x 8191 x 2048 channels 29.5 us for 134 MB (4.6 TB/s), 23 us for the
+// 110 MB of padded sequences with 64% of these tokens, the zeros behind them written; backward
+// of 4 x 2048 x 2048 31 us for 101 MB (3.3 TB/s; the launch of the sums is 4 of them; the vector ALUs
+// are 55% busy with silu and its derivative).  Its walks of 32 tokens bring two waves a SIMD where
+// registers allow three: walks of 24, 22 and 16 tokens bring more, read more rows twice and leave
+// more partial sums, and take 33.7, 34.2 and 36.4 us (fp32 53 us with 32 tokens, 57 to 65 with those).
 
 #include "block.h"
 #include "launch.h"

@@ -13,11 +13,10 @@
 // through LDS, and a second launch adds the workgroups' partial sums in a fixed order.
 //
 // Measured: forward, 16384 x 2048 bf16, 134 MB in 30 us (4.4 TB/s; a large copy reaches
-// 5.1); backward, 8200 x 1111 f32, 109 MB in 26 us, the column sums included.
-//
-// Measured: forward, 16384 x 2048 bf16, 134 MB in 30 us (4.4 TB/s; a large copy reaches
-// 5.1); backward, 8191 x 1111 f32, 109 MB in 26 us, 2.5 of them the column sums; backward,
-// 16384 x 2048 bf16, 55 us.
+// 5.1); backward, 8200 x 1111 f32, 109 MB in 26 us, 22 of them this kernel and 5 the column
+// sums (profiled); backward, 16384 x 2048 and 4096 x 8192 bf16, 201 MB in 54 us (49 and 5), which
+// wait 62% of the waves' time: a workgroup has one row ahead in flight, and leaves and reads
+// again 13 to 17 MB of partial sums.
 
 #include "block.h"
 #include "launch.h"

@@ -11,9 +11,9 @@
 // sum of its dt (the segment's whole decay is exp(A sum dt)), a small kernel composes the
 // entry states, and the main pass walks all segments at once.
 //
-// Measured, S = 16, bf16, gated: 4 x 2048 x 2048 channels 124 us (first pass 55, composition 9,
-// main pass 71), 1 x 16384 x 2048 228 us; the vector ALUs are busy 65-74% of the first pass
-// and 81% of the main pass, and issue matrix instructions in much of the rest.  An
+// Measured, S = 16, bf16, gated: 4 x 2048 x 2048 channels 125 us (first pass 50, composition 9,
+// main pass 66), 1 x 16384 x 2048 230 us (95, 11 and 123); the vector ALUs are busy 65-75% of the
+// first pass and 72-80% of the main pass, and issue matrix instructions in much of the rest.  An
 // exponential costs as much issue time as three multiply-adds, so the pass cannot be much
 // shorter than its instructions.
 

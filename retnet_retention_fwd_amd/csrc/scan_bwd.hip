@@ -24,9 +24,9 @@
 // one walks the adjoint back through each from zero, and a small kernel composes both into
 // the states that enter the segments from either side.
 //
-// Measured, S = 16, bf16, gated: 4 x 2048 x 2048 channels 373 us, of which first passes 112,
-// composition 10, main pass 250 (vector ALUs busy 91%; 51 KB of LDS and 168 registers leave
-// three workgroups a CU, and parts of eight tokens do not fit those registers), sums 16.
+// Measured, S = 16, bf16, gated: 4 x 2048 x 2048 channels 374 us, of which first passes 101,
+// composition 10, main pass 250 (vector ALUs busy 92%; 51 KB of LDS and 168 registers leave
+// three workgroups a CU, and parts of eight tokens do not fit those registers), sums 12.
 
 #include "scan.h"
 
@@ -241,8 +241,8 @@ __device__ __forceinline__ void walk_back(const ScanArgs& a, const ScanPlan& pl,
 }
 
 // Both walks in one launch: neither needs the other, and together they bring each SIMD the
-// waves that keep its vector ALU busy (142 us one behind the other in a training step's
-// backward, 120 us together, with the composition).
+// waves that keep its vector ALU busy (22 us less than one behind the other in a training step's
+// backward, where they take 101 us together).
 // ALL: S = SP; its rows are then stored without tests (4 x 2048 x 512 channels, S = 64: 133 us against 165).
 template <typename T, int SP, bool ALL>
 __global__ __launch_bounds__(kScanThreads, SP <= 16 ? 4 : 2) void scan_first_kernel(ScanArgs a, ScanPlan pl) {
