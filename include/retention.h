@@ -280,7 +280,8 @@ int retention_abi_version(void);
  * Kinds: 0 matrix-core chunkwise pass, 1 its segment-state pre-pass, 2 its segment
  * scan, 3 generic chunkwise kernel, 4 decode step, 5 state copy (empty sequence), 6 layer
  * normalisation, 7 rotary positions, 8 causal convolution, 9 selective scan, 10 its passes
- * over segments and tiles before that, 11 sums of partial gradients.
+ * over segments and tiles before that, 11 sums of partial gradients and of split products, 12
+ * projections, 13 their passes over single tensors, 14 head norms with rotary positions.
  * Errors: RETN_ERR_SHAPE (nkinds < 0), RETN_ERR_NULL, RETN_ERR_HIP.
  */
 retn_status retention_profile_enable(int on);
@@ -520,6 +521,132 @@ retn_status selective_scan_step(const void* x, const void* dt, const float* A, c
                                 long long lddt, long long ldz, long long ldb, long long ldc,
                                 int B, int D, int G, int S, int softplus, retn_dtype dtype,
                                 void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Projections of a block: the matrix product with what follows it, the gated feed-forward
+ * block, and the norms of queries and keys between a projection and the mixer.
+ *
+ * Conventions as above, with:
+ *   Types      x, weights, residuals, outputs and their gradients have one type, `dtype`; biases
+ *              (`bdtype`) and the weights of the head norms (`wdtype`) are fp32 or of that type.
+ *              Products are summed in fp32 by the matrix cores.  bf16: besides the outputs, what
+ *              one product hands to the next (the gated product, gradients behind an activation)
+ *              is rounded to bf16, which is what the matrix cores take.
+ *   Layout     x is [rows, K], ldx elements from row to row (a column slice of a wider projection
+ *              is taken in place); weights are [out, in]; all else is contiguous.  Any element
+ *              alignment; operands whose rows all start on 16-byte boundaries are read in place,
+ *              others are laid out anew in the workspace first.  `aligned` of a workspace query:
+ *              whether the pointers of x, the weights and grad_y, x's row stride and all widths
+ *              are multiples of 16 bytes (0 is always enough).
+ *   Limits     rows < 2^28, widths and row strides <= 2^20, a tensor's elements < 2^34; else
+ *              RETN_ERR_UNSUPPORTED.
+ * All results are the same from call to call (no atomics).
+ */
+typedef enum {
+    RETN_ACT_NONE = 0,
+    RETN_ACT_RELU = 1,
+    RETN_ACT_GELU = 2,        /* z times the normal distribution function */
+    RETN_ACT_GELU_TANH = 3,   /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    RETN_ACT_SILU = 4,
+    /* Not activations: every int is a valid value of the type (others are rejected with
+       RETN_ERR_SHAPE). */
+    RETN_ACT_RANGE_MIN_ = -2147483647 - 1,
+    RETN_ACT_RANGE_MAX_ = 2147483647
+} retn_activation;
+
+/*
+ * Projection: z = x weight^T + bias,  y = act(z) + residual
+ *   weight [N, K];  bias [N], residual [rows, N], each optional;  y [rows, N]
+ *   pre       optional output [rows, N]: z, what linear_bwd takes for an activation
+ *   y may be exactly the residual; no other output may overlap an input or another output.
+ *   workspace linear_workspace_bytes(...), 16-byte aligned
+ */
+retn_status linear_fwd(const void* x, long long ldx, const void* weight, const void* bias,
+                       const void* residual, void* y, void* pre, long long rows, int N, int K,
+                       retn_activation activation, retn_dtype dtype, retn_dtype bdtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+size_t linear_workspace_bytes(long long rows, int N, int K, retn_dtype dtype, int aligned);
+
+/*
+ * Backward of linear_fwd for the gradient grad_y [rows, N] of y (which is the residual's too):
+ *     gz = grad_y act'(pre),  grad_x = gz weight,  grad_weight = gz^T x,  grad_bias = sum of gz
+ *   pre          the forward's; NULL without an activation
+ *   grad_x [rows, K], grad_weight [N, K], grad_bias [N] of bdtype: each optional
+ */
+retn_status linear_bwd(const void* x, long long ldx, const void* weight, const void* pre,
+                       const void* grad_y, void* grad_x, void* grad_weight, void* grad_bias,
+                       long long rows, int N, int K, retn_activation activation,
+                       retn_dtype dtype, retn_dtype bdtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
+size_t linear_bwd_workspace_bytes(long long rows, int N, int K, retn_activation activation,
+                                  retn_dtype dtype, int aligned);
+
+/*
+ * Gated feed-forward block: g = x w_gate^T, u = x w_up^T, y = (act(g) * u) w_down^T + residual
+ *   x [rows, D];  w_gate, w_up [F, D];  w_down [D, F];  residual [rows, D] optional;  y [rows, D]
+ *   gate, up  optional outputs [rows, F] (both or neither): g and u, what gated_ffn_bwd takes
+ *   y may be exactly the residual; no other overlap.
+ */
+retn_status gated_ffn_fwd(const void* x, long long ldx, const void* w_gate, const void* w_up,
+                          const void* w_down, const void* residual, void* y, void* gate,
+                          void* up, long long rows, int D, int F, retn_activation activation,
+                          retn_dtype dtype, void* workspace, size_t workspace_bytes,
+                          void* stream);
+size_t gated_ffn_workspace_bytes(long long rows, int D, int F, retn_dtype dtype, int aligned);
+
+/*
+ * Backward of gated_ffn_fwd for the gradient grad_y [rows, D] of y (which is the residual's too):
+ *     gh = grad_y w_down,  gu = gh act(g),  gg = gh u act'(g),
+ *     grad_x = gg w_gate + gu w_up,  grad_w_gate = gg^T x,  grad_w_up = gu^T x,
+ *     grad_w_down = grad_y^T (act(g) u)
+ *   grad_x [rows, D] optional; the weights' gradients: all three or none
+ */
+retn_status gated_ffn_bwd(const void* x, long long ldx, const void* w_gate, const void* w_up,
+                          const void* w_down, const void* gate, const void* up,
+                          const void* grad_y, void* grad_x, void* grad_w_gate,
+                          void* grad_w_up, void* grad_w_down, long long rows, int D, int F,
+                          retn_activation activation, retn_dtype dtype, void* workspace,
+                          size_t workspace_bytes, void* stream);
+size_t gated_ffn_bwd_workspace_bytes(long long rows, int D, int F, retn_dtype dtype, int aligned);
+
+/*
+ * Root-mean-square norm of each head's row and rotary positions in one pass:
+ *     r = 1 / sqrt(mean(x^2) + eps) over the d elements,  out = scale * turn(x r weight)
+ * with the turn, the tensors' strides, the table and the positions of rotary_fwd.
+ *   q_weight, k_weight  [d] of wdtype, each optional (NULL: ones), one for all heads
+ *   strides             host array of 12, as rotary_fwd's;  eps >= 0
+ *   An output may be exactly its input; no other overlap.
+ *   Limits as rotary_fwd's.
+ */
+retn_status head_norm_rotary_fwd(const void* q, const void* k, void* out_q, void* out_k,
+                                 const long long* strides, const void* q_weight,
+                                 const void* k_weight, const float* table, long long table_len,
+                                 const long long* positions, int positions_per_batch,
+                                 long long first, int B, int Hq, int Hk, int N, int d, int rot,
+                                 int interleaved, float eps, float q_scale, float k_scale,
+                                 retn_dtype dtype, retn_dtype wdtype, void* stream);
+
+/*
+ * Backward of head_norm_rotary_fwd for the gradients grad_q, grad_k of its outputs: with
+ * g = scale * turn^T(grad), xh = x r, v = g weight:  out = r (v - xh mean(v xh)),
+ * grad_weight = sum of g xh over all rows.
+ *   strides     host array of 18: batch, head and token strides of q, grad_q, out_q, k, grad_k,
+ *               out_k.  An output may be exactly its gradient; no other overlap.
+ *   grad_q_weight, grad_k_weight  [d] of wdtype, each optional
+ *   workspace   head_norm_rotary_bwd_workspace_bytes(...), 16-byte aligned; needed only where a
+ *               weight's gradient is given
+ */
+retn_status head_norm_rotary_bwd(const void* q, const void* k, const void* grad_q,
+                                 const void* grad_k, void* out_q, void* out_k,
+                                 const long long* strides, const void* q_weight,
+                                 const void* k_weight, void* grad_q_weight,
+                                 void* grad_k_weight, const float* table, long long table_len,
+                                 const long long* positions, int positions_per_batch,
+                                 long long first, int B, int Hq, int Hk, int N, int d, int rot,
+                                 int interleaved, float eps, float q_scale, float k_scale,
+                                 retn_dtype dtype, retn_dtype wdtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+size_t head_norm_rotary_bwd_workspace_bytes(int d);
 
 #ifdef __cplusplus
 }

@@ -39,7 +39,6 @@ SIGNATURES = {
 }
 
 _Strides = _ll * 12
-_bound = {}
 _HERE = contextlib.nullcontext()
 _T = None
 
@@ -53,15 +52,22 @@ def _torch():
     return _T
 
 
-def _fn(name):
-    """The library's function with its argument types, looked up once."""
-    f = _bound.get(name)
-    if f is None:
-        f = getattr(lib(), name)
-        f.argtypes = SIGNATURES[name]
-        f.restype = _sz if name.endswith("_bytes") else _i
-        _bound[name] = f
-    return f
+def _binder(signatures):
+    """The library's functions with these argument types, each looked up once."""
+    bound = {}
+
+    def fn(name):
+        f = bound.get(name)
+        if f is None:
+            f = getattr(lib(), name)
+            f.argtypes = signatures[name]
+            f.restype = _sz if name.endswith("_bytes") else _i
+            bound[name] = f
+        return f
+    return fn
+
+
+_fn = _binder(SIGNATURES)
 
 
 def _ptr(t):

@@ -59,11 +59,23 @@ EXPORTED = (
     "selective_scan_bwd",
     "selective_scan_bwd_workspace_bytes",
     "selective_scan_step",
+    "linear_fwd",
+    "linear_workspace_bytes",
+    "linear_bwd",
+    "linear_bwd_workspace_bytes",
+    "gated_ffn_fwd",
+    "gated_ffn_workspace_bytes",
+    "gated_ffn_bwd",
+    "gated_ffn_bwd_workspace_bytes",
+    "head_norm_rotary_fwd",
+    "head_norm_rotary_bwd",
+    "head_norm_rotary_bwd_workspace_bytes",
 )
 
 # Kernel kinds reported by retention_profile_read.
 PROFILE_KINDS = ("chunk_main", "chunk_prepass", "chunk_scan", "chunk_generic", "decode", "state_copy", "layer_norm",
-                 "rotary", "causal_conv", "selective_scan", "selective_scan_prepass", "gradient_sums")
+                 "rotary", "causal_conv", "selective_scan", "selective_scan_prepass", "gradient_sums",
+                 "projection", "projection_pass", "head_norm_rotary")
 
 
 class RetentionError(RuntimeError):

@@ -1,0 +1,689 @@
+// Matrix products of a block's projections: C = A B with fp32 accumulation on the matrix
+// cores and what follows a projection (bias, activation, residual, the gated product and its
+// gradients) applied to the sums before they are stored.
+//
+// A workgroup owns a BM x BN tile of C and walks the reduction in steps of 128 bytes a row
+// (64 bf16 or 32 fp32 elements).  Both operands' step lies in LDS twice: one stage is read
+// while the other is filled by asynchronous copies from memory, whose instructions go out one
+// at a time between the matrix instructions.  A step has two halves.  While the first half's
+// products run, the second half's fragments are read; then the workgroup meets (the step has
+// been read by all, the next step has landed), and while the second half's products run, the
+// next step's first fragments are read and the step after it is fetched into the stage that
+// is free.  So the barrier is the only place at which the matrix cores may run dry.
+//
+// Operands come in either order: reduction-major rows give 16-byte fragments as they lie;
+// output-major rows (a transposed operand: a weight in the gradient of x, both operands in
+// the gradient of a weight) are read by the transposing LDS loads (bf16), or by single words
+// (fp32, whose matrix instructions are slow enough to hide them), so no operand is ever
+// transposed in memory.
+
+#include "act.h"
+#include "cdna4.h"
+#include "common.h"
+#include "launch.h"
+#include "proj.h"
+#include "vec_io.h"
+
+#include <algorithm>
+#include <mutex>
+
+namespace retn {
+namespace {
+
+constexpr uint32_t kOutside = 0x80000000u;   // a byte offset past every buffer resource here
+
+typedef float f32x4u_t __attribute__((ext_vector_type(4)));
+
+// c += a b over one fragment: 16 x 16 sums, 32 (bf16) or 16 (fp32) elements of the reduction.
+// Lane (g, l) = (lane / 16, lane % 16) brings row l of a and column l of b, 16 bytes of the
+// reduction from 16 g on, and holds columns ... of c as the matrix instructions do; which
+// elements meet in one instruction is the same for both operands, so any order will do.
+template <typename T>
+__device__ __forceinline__ f32x4_t frag_mul(u16x8_t a, u16x8_t b, f32x4_t c) {
+    if constexpr (sizeof(T) == 2) {
+        return mfma16(a, b, c);
+    } else {
+        const f32x4_t x = __builtin_bit_cast(f32x4_t, a), y = __builtin_bit_cast(f32x4_t, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[j], y[j], c, 0, 0, 0);
+        return c;
+    }
+}
+
+// An operand's tile in LDS: R rows of the output.
+//   RED:  [R][128 bytes of the reduction]; the 16-byte unit u of row r sits at u ^ ((r >> 1) & 7),
+//         so the 16 rows of a fragment read cover all banks.
+//   else: [elements of the step][R elements]; unit u of row r sits at u ^ swz(r).  A transposing
+//         read of 32 lanes takes 32 bytes each from rows {0..3, 8..11} (plus 4, or 16): these
+//         are spread over the 256 bytes of all banks; fp32 words come as 64 bytes from every fourth row.
+template <typename T, bool RED, int R, int NW>
+struct Side {
+    static constexpr int kEs = sizeof(T), kEpu = 16 / kEs, kStep = 128 / kEs;
+    static constexpr int kRow = R * kEs;              // bytes of a row, output-major
+    static constexpr int kCopies = R / 8 / NW;        // copies of 1 KB a wave makes for a step
+    static constexpr int kBytes = R * 128;
+    static_assert(RED || kRow >= 256, "the swizzle spans 256 bytes");
+
+    __device__ __forceinline__ static int swz(int r) {
+        return kEs == 2 ? 2 * ((r & 3) | (((r >> 3) & 1) << 2)) : ((r >> 2) & 3) << 2;
+    }
+
+    uint32_t off[kCopies];      // lane's byte offset of each copy, from the tile's start
+    uint32_t fr[RED ? 2 : (kEs == 2 ? 8 : 4)];   // lane's LDS offset of fragments
+    int unit;                   // RED: the unit that a lane copies (the same in every copy)
+
+    // T0: the wave's first 16-row block; PAIRS: rows alternate in blocks of 16 between two sources.
+    template <bool PAIRS>
+    __device__ __forceinline__ void init(int wave, int lane, int t0, int ld) {
+        const int l16 = lane & 15, g4 = lane >> 4;
+        unit = 0;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int c = wave + NW * i;
+            if constexpr (RED) {
+                const int r = c * 8 + lane / 8;
+                unit = (lane & 7) ^ ((r >> 1) & 7);
+                static_assert(NW % 2 == 0, "copies of a wave start at rows of one parity of 8");
+                const int src = PAIRS ? (c >> 2) * 16 + (c & 1) * 8 + lane / 8 : r;
+                off[i] = static_cast<uint32_t>(src) * ld * kEs + unit * 16;
+            } else {
+                const int o = c * 1024 + lane * 16, r = o / kRow, u = ((o % kRow) >> 4) ^ swz(r);
+                off[i] = static_cast<uint32_t>(r) * ld * kEs + u * 16;
+            }
+        }
+        if constexpr (RED) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+                fr[ks] = (t0 * 16 + l16) * 128 + (((ks * 4 + g4) ^ ((l16 >> 1) & 7)) << 4);
+        } else if constexpr (kEs == 2) {
+            const int r = 8 * g4 + (l16 >> 2);
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                fr[t] = r * kRow + (((2 * (t0 + t) + ((l16 & 3) >> 1)) ^ swz(r)) << 4) + (l16 & 1) * 8;
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) fr[t] = 4 * g4 * kRow + (((4 * (t0 + t) + (l16 >> 2)) ^ (g4 << 2)) << 4) + (l16 & 3) * 4;
+        }
+    }
+    // Fragment of the wave's row block t, half ks of the step, from the tile at LDS address `at`.
+    __device__ __forceinline__ u16x8_t read(uint32_t at, int t, int ks) const {
+        if constexpr (RED) {
+            return lds16a(at + fr[ks] + t * 16 * 128);
+        } else if constexpr (kEs == 2) {
+            const uint32_t p = at + fr[t] + ks * 32 * kRow;
+            return cat(lds_tra(p), lds_tra(p + 4 * kRow));
+        } else {
+            typedef __attribute__((address_space(3))) const float lds_f32_t;
+            const uint32_t p = at + fr[t & 3] + (t >> 2) * 256 + ks * 16 * kRow;
+            f32x4_t v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = *(lds_f32_t*)(static_cast<size_t>(p + j * kRow));
+            return __builtin_bit_cast(u16x8_t, v);
+        }
+    }
+};
+
+// Where a step's copies come from: the resource, its scalar offset, and (RED) how many units of
+// the step hold elements of the reduction.
+struct Source {
+    u32x4_t rs;
+    uint32_t soff;
+    int units;
+};
+template <typename T, bool RED>
+__device__ __forceinline__ Source step_source(const void* base, long long ld, int rows, int cols, int red, int red_rows, int kt) {
+    constexpr int kEs = sizeof(T), kStep = 128 / kEs, kEpu = 16 / kEs;
+    Source s;
+    const char* p = static_cast<const char*>(base);
+    if constexpr (RED) {
+        s.rs = make_rsrc(p, static_cast<uint32_t>(((rows - 1) * ld + red) * kEs));
+        s.soff = kt * 128;
+        s.units = (red - kt * kStep + kEpu - 1) / kEpu;
+    } else {
+        const int left = min(kStep, red_rows - kt * kStep), width = (cols + kEpu - 1) / kEpu * kEpu;
+        s.rs = make_rsrc(p + static_cast<long long>(kt) * kStep * ld * kEs, static_cast<uint32_t>(((left - 1) * ld + width) * kEs));
+        s.soff = 0;
+        s.units = 8;
+    }
+    return s;
+}
+
+// ---- what happens to the sums -------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        const Raw<T, 8> r = raw_load_n<T, 8>(p, left);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = up(r.v[i]);
+    } else {
+        const Raw<T, 4> r = raw_load_n<T, 4>(p, left), q = raw_load_n<T, 4>(p + 4, left - 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = r.v[i];
+            v[i + 4] = q.v[i];
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8], int left) {
+    if constexpr (sizeof(T) == 2) {
+        store_n<T, 8>(p, v, left);
+    } else {
+        const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+        store_n<T, 4>(p, lo, left);
+        store_n<T, 4>(p + 4, hi, left - 4);
+    }
+}
+
+// Eight adjacent columns n .. n + 7 of row m (`v`, and `w`: the second projection's sums).
+template <typename T, int KIND>
+__device__ __forceinline__ void finish8(const ProjEpi& e, const ProjGroup& g, int m, int n, float (&v)[8], float (&w)[8]) {
+    const int left = g.N - n;
+    const size_t at = static_cast<size_t>(m) * g.N + n;
+    T* c = static_cast<T*>(g.c) + static_cast<size_t>(m) * g.ldc + n;
+    if constexpr (KIND == kProjLinear) {
+        if (e.bias != nullptr) {
+            float b[8];
+            if (e.bias_f32)
+                load8<float>(static_cast<const float*>(e.bias) + n, left, b);
+            else
+                load8<T>(static_cast<const T*>(e.bias) + n, left, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += b[i];
+        }
+        if (e.pre != nullptr) store8<T>(static_cast<T*>(e.pre) + at, v, left);
+        if (e.act != RETN_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], e.act);
+        }
+        if (e.res != nullptr) {
+            float r[8];
+            load8<T>(static_cast<const T*>(e.res) + at, left, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
+        }
+        store8<T>(c, v, left);
+    } else if constexpr (KIND == kProjGated) {
+        // (columns of a padded product past gate's and up's are zero: both sums are)
+        const size_t ga = static_cast<size_t>(m) * e.gate_ld + n;
+        if (e.gate != nullptr) store8<T>(static_cast<T*>(e.gate) + ga, v, e.gate_n - n);
+        if (e.up != nullptr) store8<T>(static_cast<T*>(e.up) + ga, w, e.gate_n - n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], e.act) * w[i];
+        store8<T>(c, v, left);
+    } else {
+        const size_t ga = static_cast<size_t>(m) * e.gate_ld + n, ca = static_cast<size_t>(m) * g.ldc + n;
+        float x[8], u[8], h[8], gx[8];
+        load8<T>(static_cast<const T*>(e.gate) + ga, e.gate_n - n, x);
+        load8<T>(static_cast<const T*>(e.up) + ga, e.gate_n - n, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float a;
+            const float s = act_slope(x[i], e.act, a);
+            h[i] = a * u[i];
+            gx[i] = v[i] * u[i] * s;
+            v[i] = v[i] * a;
+        }
+        if (e.ggate != nullptr) store8<T>(static_cast<T*>(e.ggate) + ca, gx, left);
+        if (e.gup != nullptr) store8<T>(static_cast<T*>(e.gup) + ca, v, left);
+        if (e.prod != nullptr) store8<T>(static_cast<T*>(e.prod) + ca, h, left);
+    }
+}
+
+__device__ __forceinline__ int round8(int n) { return (n + 7) & ~7; }
+
+// ---- the product ----------------------------------------------------------------------------------
+template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int KIND>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void proj_kernel(const ProjArgs p) {
+    constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+    static_assert(TN == 4 && TM <= 8, "a wave's tile is up to 128 x 64");
+    constexpr bool PAIRS = KIND == kProjGated;
+    typedef Side<T, AR, BM, NW> A;
+    typedef Side<T, BR, BN, NW> B;
+    constexpr int kStage = A::kBytes + B::kBytes, kEs = sizeof(T), kStep = 128 / kEs;
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l16 = lane & 15, g4 = lane >> 4, wm = wave / WN, wn = wave % WN;
+
+    // XCD-aware order: launch ids rotate over the 8 XCDs; each XCD gets a contiguous range of
+    // tiles, walked in bands of rows so that the tiles in flight share both operands in its L2
+    const int total = p.tiles * p.splits;
+    int id = blockIdx.x;
+    {
+        const int x = id & 7, q = total >> 3, r = total & 7;
+        id = x * q + min(x, r) + (id >> 3);
+    }
+    const int split = id / p.tiles;
+    int t = id % p.tiles, gi = 0;
+    if (p.ngroups > 1 && t >= p.g[0].end) gi = p.ngroups > 2 && t >= p.g[1].end ? 2 : 1;
+    const ProjGroup& g = p.g[gi];
+    if (gi > 0) t -= p.g[gi - 1].end;
+    const int tiles_n = g.tiles_n;
+    constexpr int kCols = PAIRS ? BN / 2 : BN;       // columns of C of a tile
+    const int tiles_m = (g.M + BM - 1) / BM;
+    const int per = p.band * tiles_n, b0 = t / per, rem = t % per, brows = min(p.band, tiles_m - b0 * p.band);
+    const int m0 = (b0 * p.band + rem % brows) * BM, n0 = (rem / brows) * kCols;
+
+    A sa;
+    B sb;
+    sa.template init<false>(wave, lane, wm * TM, g.lda);
+    sb.template init<PAIRS>(wave, lane, wn * TN, g.ldb);
+
+    const int nk1 = (p.red + kStep - 1) / kStep;
+    const int s0 = split * p.per_split, s1 = min(s0 + p.per_split, nk1 * p.phases);
+    const int arows = min(BM, g.M - m0), bcols = min(kCols, g.bn - n0);
+    const size_t aoff = static_cast<size_t>(m0) * (AR ? g.lda : 1), boff = static_cast<size_t>(n0) * (BR ? g.ldb : 1);
+    auto a_src = [&](int kt) {
+        const bool second = kt >= nk1;
+        return step_source<T, AR>(static_cast<const T*>(second ? g.a2 : g.a) + aoff, g.lda, arows, g.M - m0, p.red,
+                                  p.red_rows, second ? kt - nk1 : kt);
+    };
+    auto b_src = [&](int kt) {
+        // (pairs: a wave's copies all belong to one of the two projections)
+        const bool second = PAIRS ? ((wave >> 1) & 1) != 0 : kt >= nk1;
+        return step_source<T, BR>(static_cast<const T*>(second ? g.b2 : g.b) + boff, g.ldb, bcols, g.bn - n0, p.red,
+                                  p.red_rows, !PAIRS && second ? kt - nk1 : kt);
+    };
+    const uint32_t lds0 = lds_addr_of(smem);
+    auto copy_a = [&](const Source& s, int i, uint32_t at) {
+        const uint32_t o = AR && sa.unit >= s.units ? kOutside : sa.off[i];
+        buf2lds16(s.rs, o, s.soff, at + (wave + NW * i) * 1024);
+    };
+    auto copy_b = [&](const Source& s, int i, uint32_t at) {
+        const uint32_t o = BR && sb.unit >= s.units ? kOutside : sb.off[i];
+        buf2lds16(s.rs, o, s.soff, at + A::kBytes + (wave + NW * i) * 1024);
+    };
+
+    f32x4_t acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    if (s0 < s1) {
+        constexpr int kCopies = A::kCopies + B::kCopies;
+        {
+            const Source ssa = a_src(s0), ssb = b_src(s0);
+#pragma unroll
+            for (int i = 0; i < A::kCopies; ++i) copy_a(ssa, i, lds0);
+#pragma unroll
+            for (int i = 0; i < B::kCopies; ++i) copy_b(ssb, i, lds0);
+        }
+        if (s0 + 1 < s1) {
+            const Source ssa = a_src(s0 + 1), ssb = b_src(s0 + 1);
+#pragma unroll
+            for (int i = 0; i < A::kCopies; ++i) copy_a(ssa, i, lds0 + kStage);
+#pragma unroll
+            for (int i = 0; i < B::kCopies; ++i) copy_b(ssb, i, lds0 + kStage);
+            wait_vmcnt<kCopies>();
+        } else {
+            wait_vmcnt<0>();
+        }
+        lds_barrier();
+        u16x8_t fa[2][TM], fb[2][TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[0][j] = sb.read(lds0 + A::kBytes, j, 0);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[0][i] = sa.read(lds0, i, 0);
+        uint32_t cur = lds0, oth = lds0 + kStage;
+        for (int kt = s0; kt < s1; ++kt) {
+            // first half's products; the second half's fragments come in
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                if (i == 0) {
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) fb[1][j] = sb.read(cur + A::kBytes, j, 1);
+                }
+                fa[1][i] = sa.read(cur, i, 1);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = frag_mul<T>(fb[0][j], fa[0][i], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            wait_vmcnt<0>();     // the next step has landed for this wave,
+            lds_barrier();       // and for all; all have read this step
+            const bool more = kt + 2 < s1, next = kt + 1 < s1;
+            Source ssa{}, ssb{};
+            if (more) {
+                ssa = a_src(kt + 2);
+                ssb = b_src(kt + 2);
+            }
+            // second half's products; the next step's first fragments, the copies of the one after
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                constexpr int kPer = (kCopies + TM - 1) / TM;
+                if (more) {
+#pragma unroll
+                    for (int c = i * kPer; c < (i + 1) * kPer && c < kCopies; ++c) {
+                        if (c < A::kCopies)
+                            copy_a(ssa, c, cur);
+                        else
+                            copy_b(ssb, c - A::kCopies, cur);
+                    }
+                }
+                if (next) {
+                    if (i == 0) {
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) fb[0][j] = sb.read(oth + A::kBytes, j, 0);
+                    }
+                    fa[0][i] = sa.read(oth, i, 0);
+                }
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = frag_mul<T>(fb[1][j], fa[1][i], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const uint32_t s = cur;
+            cur = oth;
+            oth = s;
+        }
+    }
+    __syncthreads();   // the stages become the waves' turning places
+
+    // The sums of 16 rows at a time go through LDS, so that a lane holds eight adjacent columns
+    // of a row and eight lanes a row's 64: whole lines to load and store.
+    constexpr int kPitch = 64 + 4;
+    float* const turn = reinterpret_cast<float*>(smem) + wave * 16 * kPitch;
+    const int np = round8(g.N);
+    constexpr int kPass = PAIRS ? 1 : 2;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4_t*>(turn + l16 * kPitch + 16 * j + 4 * g4) = acc[i][j];
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int q = 0; q < kPass; ++q) {
+            const int row = PAIRS ? lane >> 2 : q * 8 + (lane >> 3);
+            const int u = PAIRS ? lane & 3 : lane & 7;
+            const float* src = turn + row * kPitch + (PAIRS ? (u >> 1) * 32 + (u & 1) * 8 : u * 8);
+            float v[8], w[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const f32x4_t x = *reinterpret_cast<const f32x4_t*>(src + 4 * k);
+                f32x4_t y{};
+                if (PAIRS) y = *reinterpret_cast<const f32x4_t*>(src + 16 + 4 * k);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    v[4 * k + r] = x[r];
+                    w[4 * k + r] = y[r];
+                }
+            }
+            const int m = m0 + (wm * TM + i) * 16 + row, n = n0 + wn * (PAIRS ? 32 : 64) + u * 8;
+            if (m >= g.M || n >= g.N) continue;
+            if (p.splits > 1) {
+                const size_t plane = static_cast<size_t>(g.M) * np;
+                float* o = p.part + g.part + split * plane * (PAIRS ? 2 : 1) + static_cast<size_t>(m) * np + n;
+                store8<float>(o, v, 8);
+                if (PAIRS) store8<float>(o + plane, w, 8);
+            } else {
+                finish8<T, KIND>(p.e, g, m, n, v, w);
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+}
+
+// Sums of split reductions, in the order of the splits.
+template <typename T, int KIND>
+__global__ __launch_bounds__(256) void proj_join_kernel(const ProjArgs p) {
+    const ProjGroup& g = p.g[blockIdx.y];
+    const int np = round8(g.N), units = np / 8;
+    const size_t plane = static_cast<size_t>(g.M) * np, total = static_cast<size_t>(g.M) * units;
+    for (size_t e = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; e < total; e += static_cast<size_t>(gridDim.x) * 256) {
+        const int m = static_cast<int>(e / units), n = static_cast<int>(e % units) * 8;
+        const float* src = p.part + g.part + static_cast<size_t>(m) * np + n;
+        float v[8] = {}, w[8] = {};
+#pragma unroll 4
+        for (int s = 0; s < p.splits; ++s) {
+            float x[8];
+            load8<float>(src, 8, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += x[i];
+            src += plane;
+            if (KIND == kProjGated) {
+                load8<float>(src, 8, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] += x[i];
+                src += plane;
+            }
+        }
+        finish8<T, KIND>(p.e, g, m, n, v, w);
+    }
+}
+
+// ---- plan ---------------------------------------------------------------------------------------
+struct Tile {
+    int bm, bn, slots;     // workgroups of the chip at a time
+    double rate;           // of the chip's matrix rate that the main loop reaches
+};
+constexpr Tile kTiles[2] = {{256, 256, 256, 1.0}, {128, 128, 512, 0.75}};
+
+// Sets tiles, splits and bands; returns the tile's number.  Estimated time: rounds of
+// workgroups, each its steps and a fixed part, then the join's traffic.
+int plan(ProjArgs& a, ProjKind kind, bool bf16) {
+    const int step = bf16 ? 64 : 32;
+    const int steps = (a.red + step - 1) / step * a.phases;
+    int best = 0, best_splits = 1;
+    double best_t = 1e30;
+    for (int c = 0; c < 2; ++c) {
+        const Tile& t = kTiles[c];
+        const int cols = kind == kProjGated ? t.bn / 2 : t.bn;
+        double tiles = 0, out = 0;
+        for (int i = 0; i < a.ngroups; ++i) {
+            tiles += static_cast<double>((a.g[i].M + t.bm - 1) / t.bm) * ((a.g[i].N + cols - 1) / cols);
+            out += static_cast<double>(a.g[i].M) * a.g[i].N * (kind == kProjGated ? 2 : 1);
+        }
+        // microseconds of a step in a full chip: its matrix instructions at 1.4 (0.13) PFLOP/s
+        const double us = 2.0 * t.bm * t.bn * step * t.slots / (t.rate * (bf16 ? 1.4e9 : 0.13e9));
+        for (int s = 1; s <= 16 && s <= steps; ++s) {
+            if (s > 1 && tiles * s > 2 * t.slots) break;
+            const int per = (steps + s - 1) / s;
+            if ((steps + per - 1) / per != s) continue;
+            const double rounds = ceil(tiles * s / t.slots);
+            double time = rounds * (per * us + 2.0) + 2.0;
+            if (s > 1) time += 3.0 + out * s * 8 / 3e6;
+            if (time < best_t) {
+                best_t = time;
+                best = c;
+                best_splits = s;
+            }
+        }
+    }
+    const Tile& t = kTiles[best];
+    a.splits = best_splits;
+    a.per_split = (steps + best_splits - 1) / best_splits;
+    a.band = 8;
+    int tiles = 0;
+    size_t part = 0;
+    for (int i = 0; i < a.ngroups; ++i) {
+        ProjGroup& g = a.g[i];
+        const int cols = kind == kProjGated ? t.bn / 2 : t.bn;
+        g.tiles_n = (g.N + cols - 1) / cols;
+        tiles += (g.M + t.bm - 1) / t.bm * g.tiles_n;
+        g.end = tiles;
+        g.part = part;
+        part += static_cast<size_t>(a.splits) * g.M * ((g.N + 7) & ~7) * (kind == kProjGated ? 2 : 1);
+    }
+    a.tiles = tiles;
+    return best;
+}
+
+template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int KIND>
+hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
+    constexpr int lds = 2 * (BM + BN) * 128;
+    static std::once_flag attr_once;   // thread-safe one-time init of the LDS limit
+    std::call_once(attr_once, [] {
+        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&proj_kernel<T, AR, BR, BM, BN, WM, WN, KIND>),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    });
+    {
+        ProfScope prof(kProfProj, st);
+        hipLaunchKernelGGL((proj_kernel<T, AR, BR, BM, BN, WM, WN, KIND>), dim3(a.tiles * a.splits), dim3(64 * WM * WN), lds,
+                           st, a);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    size_t most = 0;
+    for (int i = 0; i < a.ngroups; ++i) most = std::max(most, static_cast<size_t>(a.g[i].M) * ((a.g[i].N + 7) / 8));
+    ProfScope prof(kProfReduce, st);
+    const unsigned blocks = static_cast<unsigned>(std::min<size_t>((most + 255) / 256, 1u << 16));
+    hipLaunchKernelGGL((proj_join_kernel<T, KIND>), dim3(blocks, a.ngroups), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename T, bool AR, bool BR, int KIND>
+hipError_t launch_sized(const ProjArgs& a, int tile, hipStream_t st) {
+    return tile == 0 ? launch_tile<T, AR, BR, 256, 256, 2, 4, KIND>(a, st)
+                     : launch_tile<T, AR, BR, 128, 128, 2, 2, KIND>(a, st);
+}
+
+template <typename T>
+hipError_t launch_typed(const ProjArgs& a, int tile, ProjKind kind, bool a_red, bool b_red, hipStream_t st) {
+    if (kind == kProjGated) return launch_sized<T, true, true, kProjGated>(a, tile, st);
+    if (kind == kProjGatedBwd) return launch_sized<T, true, false, kProjGatedBwd>(a, tile, st);
+    if (a_red) return b_red ? launch_sized<T, true, true, kProjLinear>(a, tile, st) : launch_sized<T, true, false, kProjLinear>(a, tile, st);
+    return launch_sized<T, false, false, kProjLinear>(a, tile, st);
+}
+
+// ---- packing and slopes ------------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(256) void pack_kernel(const T* src, long long lds, T* dst, long long ldd, size_t rows, int width) {
+    constexpr int V = kPack<T>;
+    const int units = static_cast<int>(ldd / V);
+    const size_t total = rows * units;
+    for (size_t e = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; e < total; e += static_cast<size_t>(gridDim.x) * 256) {
+        const size_t r = e / units;
+        const int n = static_cast<int>(e % units) * V;
+        raw_store<T, V>(dst + r * ldd + n, raw_load_n<T, V>(src + r * lds + n, width - n));
+    }
+}
+
+// Lanes of a wave lie over units of eight columns, lpr of them a row; a workgroup takes a
+// strip of 8 lpr columns and a chunk of rows, and leaves one row of partial sums.
+struct SlopePlan {
+    int lpr, strips, chunks;
+    size_t per;
+};
+SlopePlan slope_plan(size_t rows, int N) {
+    SlopePlan s;
+    s.lpr = 1;
+    while (s.lpr < 64 && s.lpr * 8 < N) s.lpr *= 2;
+    s.strips = (N + 8 * s.lpr - 1) / (8 * s.lpr);
+    const size_t at_once = 4 * (64 / s.lpr);                         // rows of a workgroup's trip
+    const size_t trips = (rows + at_once - 1) / at_once;
+    // about 2048 workgroups, eight trips at least each
+    size_t want = 2048 / s.strips;
+    if (want < 1) want = 1;
+    if (want > 512) want = 512;
+    size_t per = (trips + want - 1) / want;
+    if (per < 8) per = 8;
+    s.per = per * at_once;
+    s.chunks = static_cast<int>((rows + s.per - 1) / s.per);
+    if (s.chunks < 1) s.chunks = 1;
+    return s;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, int lpr, size_t per) {
+    __shared__ float sums[256][9];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rpw = 64 / lpr;
+    const int n = (blockIdx.x * lpr + lane % lpr) * 8, left = a.N - n;
+    const size_t r0 = blockIdx.y * per, r1 = min(r0 + per, a.rows);
+    float s[8] = {};
+    const bool pad = a.gz != nullptr && n < a.ldz;                   // columns of gz, zeros among them
+    if (left > 0 || pad) {
+        for (size_t r = r0 + wave * rpw + lane / lpr; r < r1; r += 4 * rpw) {
+            float g[8] = {};
+            if (left > 0) load8<T>(static_cast<const T*>(a.gy) + r * a.N + n, left, g);
+            if (a.pre != nullptr) {
+                float z[8] = {};
+                if (left > 0) load8<T>(static_cast<const T*>(a.pre) + r * a.N + n, left, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float v;
+                    const float d = act_slope(z[i], a.act, v);
+                    g[i] = i < left ? g[i] * d : 0.f;
+                }
+            }
+            if (pad) store8<T>(static_cast<T*>(a.gz) + r * a.ldz + n, g, static_cast<int>(a.ldz) - n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] += g[i];
+        }
+    }
+    if (a.part == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[threadIdx.x][i] = s[i];
+    __syncthreads();
+    if (threadIdx.x >= lpr) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float t = 0.f;
+        for (int k = threadIdx.x; k < 256; k += lpr) t += sums[k][i];
+        if (i < left) a.part[static_cast<size_t>(blockIdx.y) * a.N + n + i] = t;
+    }
+}
+
+}  // namespace
+
+size_t proj_partial_bytes(const ProjArgs& args, ProjKind kind, bool bf16) {
+    ProjArgs a = args;
+    (void)plan(a, kind, bf16);
+    if (a.splits == 1) return 0;
+    size_t n = 0;
+    for (int i = 0; i < a.ngroups; ++i)
+        n += static_cast<size_t>(a.splits) * a.g[i].M * ((a.g[i].N + 7) & ~7) * (kind == kProjGated ? 2 : 1);
+    return n * sizeof(float);
+}
+
+hipError_t launch_proj(ProjArgs a, ProjKind kind, bool bf16, bool a_red, bool b_red, hipStream_t st) {
+    const int tile = plan(a, kind, bf16);
+    if (a.tiles == 0) return hipSuccess;
+    return bf16 ? launch_typed<bf16_t>(a, tile, kind, a_red, b_red, st) : launch_typed<float>(a, tile, kind, a_red, b_red, st);
+}
+
+hipError_t launch_proj_pack(const void* src, long long lds, void* dst, long long ldd, size_t rows, int width, bool bf16,
+                            hipStream_t st) {
+    const size_t n = rows * static_cast<size_t>(ldd / (bf16 ? 8 : 4));
+    if (n == 0) return hipSuccess;
+    const unsigned blocks = static_cast<unsigned>(std::min<size_t>((n + 255) / 256, 1u << 14));
+    ProfScope prof(kProfProjPass, st);
+    if (bf16)
+        hipLaunchKernelGGL((pack_kernel<bf16_t>), dim3(blocks), dim3(256), 0, st, static_cast<const bf16_t*>(src), lds,
+                           static_cast<bf16_t*>(dst), ldd, rows, width);
+    else
+        hipLaunchKernelGGL((pack_kernel<float>), dim3(blocks), dim3(256), 0, st, static_cast<const float*>(src), lds,
+                           static_cast<float*>(dst), ldd, rows, width);
+    return hipGetLastError();
+}
+
+size_t slope_partial_bytes(size_t rows, int N) {
+    return static_cast<size_t>(slope_plan(rows, N).chunks) * N * sizeof(float);
+}
+
+hipError_t launch_slope(const SlopeArgs& a, hipStream_t st) {
+    const SlopePlan s = slope_plan(a.rows, a.N);
+    {
+        ProfScope prof(kProfProjPass, st);
+        const dim3 grid(s.strips, s.chunks);
+        if (a.bf16)
+            hipLaunchKernelGGL((slope_kernel<bf16_t>), grid, dim3(256), 0, st, a, s.lpr, s.per);
+        else
+            hipLaunchKernelGGL((slope_kernel<float>), grid, dim3(256), 0, st, a, s.lpr, s.per);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || a.part == nullptr) return e;
+    }
+    ColReduceArgs c{};
+    c.in = a.part;
+    c.P = s.chunks;
+    c.rows = 1;
+    c.K = 1;
+    c.D = a.N;
+    c.out0 = a.sums;
+    c.out_bf16 = a.bf16 && !a.sums_f32;
+    return launch_col_reduce(c, st);
+}
+
+}  // namespace retn
