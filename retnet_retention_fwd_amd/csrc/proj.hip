@@ -3,13 +3,15 @@
 // gradients) applied to the sums before they are stored.
 //
 // A workgroup owns a BM x BN tile of C and walks the reduction in steps of 128 bytes a row
-// (64 bf16 or 32 fp32 elements).  Both operands' step lies in LDS twice: one stage is read
-// while the other is filled by asynchronous copies from memory, whose instructions go out one
-// at a time between the matrix instructions.  A step has two halves.  While the first half's
-// products run, the second half's fragments are read; then the workgroup meets (the step has
-// been read by all, the next step has landed), and while the second half's products run, the
-// next step's first fragments are read and the step after it is fetched into the stage that
-// is free.  So the barrier is the only place at which the matrix cores may run dry.
+// (64 bf16 or 32 fp32 elements).  Both operands' step lies in LDS twice, each as two halves of
+// its rows (A: upper and lower, B: left and right), filled by asynchronous copies from memory
+// whose instructions go out one at a time between the matrix instructions.  A wave owns 16-row
+// blocks in both halves of either operand, so its tile falls into four quarters, and a step
+// goes through them: upper left, upper right, lower right, lower left.  While a quarter's
+// products run, the half that the next quarter brings in is read into registers; half of the
+// step's halves are free again after each pair of quarters, where the workgroup meets, and are
+// then filled for the step after the next.  So a copy has one to one and a half steps to
+// arrive, and the matrix cores may run dry only at two barriers a step.
 //
 // Operands come in either order: reduction-major rows give 16-byte fragments as they lie;
 // output-major rows (a transposed operand: a weight in the gradient of x, both operands in
@@ -26,6 +28,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 namespace retn {
 namespace {
@@ -50,62 +53,57 @@ __device__ __forceinline__ f32x4_t frag_mul(u16x8_t a, u16x8_t b, f32x4_t c) {
     }
 }
 
-// An operand's tile in LDS: R rows of the output.
-//   RED:  [R][128 bytes of the reduction]; the 16-byte unit u of row r sits at u ^ ((r >> 1) & 7),
-//         so the 16 rows of a fragment read cover all banks.
+// Half of an operand's tile in LDS: R rows of the output.
+//   RED:  [R][128 bytes of the reduction]; the 16-byte unit u of row r sits at u ^ swz(r), so
+//         the 16 rows of a fragment read cover all banks.
 //   else: [elements of the step][R elements]; unit u of row r sits at u ^ swz(r).  A transposing
 //         read of 32 lanes takes 32 bytes each from rows {0..3, 8..11} (plus 4, or 16): these
 //         are spread over the 256 bytes of all banks; fp32 words come as 64 bytes from every fourth row.
 template <typename T, bool RED, int R, int NW>
-struct Side {
+struct Half {
     static constexpr int kEs = sizeof(T), kEpu = 16 / kEs, kStep = 128 / kEs;
-    static constexpr int kRow = R * kEs;              // bytes of a row, output-major
-    static constexpr int kCopies = R / 8 / NW;        // copies of 1 KB a wave makes for a step
+    static constexpr int kRow = RED ? 128 : R * kEs;  // bytes of a row
     static constexpr int kBytes = R * 128;
-    static_assert(RED || kRow >= 256, "the swizzle spans 256 bytes");
+    static constexpr int kCopies = R / 8 / NW;        // copies of 1 KB a wave makes for a step
+    static constexpr int kBlocks = 4;                 // 16-row blocks that a wave may own
+    static_assert(kCopies * 8 * NW == R && (RED || kRow >= 128), "whole copies");
 
     __device__ __forceinline__ static int swz(int r) {
-        return kEs == 2 ? 2 * ((r & 3) | (((r >> 3) & 1) << 2)) : ((r >> 2) & 3) << 2;
+        if (RED) return (r >> 1) & 7;
+        if (kEs == 4) return ((r >> 2) & 3) << 2;
+        return kRow == 128 ? 2 * (((r >> 1) & 1) | (((r >> 3) & 1) << 1)) : 2 * ((r & 3) | (((r >> 3) & 1) << 2));
     }
 
-    uint32_t off[kCopies];      // lane's byte offset of each copy, from the tile's start
-    uint32_t fr[RED ? 2 : (kEs == 2 ? 8 : 4)];   // lane's LDS offset of fragments
+    uint32_t off[kCopies];      // lane's byte offset of each copy, from the half's start
+    uint32_t fr[RED ? 2 : kBlocks];   // lane's LDS offset of fragments
     int unit;                   // RED: the unit that a lane copies (the same in every copy)
 
-    // T0: the wave's first 16-row block; PAIRS: rows alternate in blocks of 16 between two sources.
-    template <bool PAIRS>
+    // t0: the wave's first 16-row block of the half.
     __device__ __forceinline__ void init(int wave, int lane, int t0, int ld) {
         const int l16 = lane & 15, g4 = lane >> 4;
         unit = 0;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            const int c = wave + NW * i;
-            if constexpr (RED) {
-                const int r = c * 8 + lane / 8;
-                unit = (lane & 7) ^ ((r >> 1) & 7);
-                static_assert(NW % 2 == 0, "copies of a wave start at rows of one parity of 8");
-                const int src = PAIRS ? (c >> 2) * 16 + (c & 1) * 8 + lane / 8 : r;
-                off[i] = static_cast<uint32_t>(src) * ld * kEs + unit * 16;
-            } else {
-                const int o = c * 1024 + lane * 16, r = o / kRow, u = ((o % kRow) >> 4) ^ swz(r);
-                off[i] = static_cast<uint32_t>(r) * ld * kEs + u * 16;
-            }
+            const int o = (wave + NW * i) * 1024 + lane * 16, r = o / kRow, u = ((o % kRow) >> 4) ^ swz(r);
+            off[i] = static_cast<uint32_t>(r) * ld * kEs + u * 16;
+            static_assert(NW % 2 == 0, "the rows of a wave's copies are alike in their swizzle");
+            if (RED) unit = u;
         }
         if constexpr (RED) {
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-                fr[ks] = (t0 * 16 + l16) * 128 + (((ks * 4 + g4) ^ ((l16 >> 1) & 7)) << 4);
+            for (int ks = 0; ks < 2; ++ks) fr[ks] = (t0 * 16 + l16) * 128 + (((ks * 4 + g4) ^ swz(l16)) << 4);
         } else if constexpr (kEs == 2) {
             const int r = 8 * g4 + (l16 >> 2);
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < kBlocks; ++t)
                 fr[t] = r * kRow + (((2 * (t0 + t) + ((l16 & 3) >> 1)) ^ swz(r)) << 4) + (l16 & 1) * 8;
         } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) fr[t] = 4 * g4 * kRow + (((4 * (t0 + t) + (l16 >> 2)) ^ (g4 << 2)) << 4) + (l16 & 3) * 4;
+            for (int t = 0; t < kBlocks; ++t)
+                fr[t] = 4 * g4 * kRow + (((4 * (t0 + t) + (l16 >> 2)) ^ (g4 << 2)) << 4) + (l16 & 3) * 4;
         }
     }
-    // Fragment of the wave's row block t, half ks of the step, from the tile at LDS address `at`.
+    // Fragment of the wave's row block t, half ks of the step, from the half at LDS address `at`.
     __device__ __forceinline__ u16x8_t read(uint32_t at, int t, int ks) const {
         if constexpr (RED) {
             return lds16a(at + fr[ks] + t * 16 * 128);
@@ -114,7 +112,7 @@ struct Side {
             return cat(lds_tra(p), lds_tra(p + 4 * kRow));
         } else {
             typedef __attribute__((address_space(3))) const float lds_f32_t;
-            const uint32_t p = at + fr[t & 3] + (t >> 2) * 256 + ks * 16 * kRow;
+            const uint32_t p = at + fr[t] + ks * 16 * kRow;
             f32x4_t v;
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = *(lds_f32_t*)(static_cast<size_t>(p + j * kRow));
@@ -123,25 +121,28 @@ struct Side {
     }
 };
 
-// Where a step's copies come from: the resource, its scalar offset, and (RED) how many units of
-// the step hold elements of the reduction.
+// Where a step's copies of a half come from: the resource (empty past the last step: zeros
+// arrive), its scalar offset, and (RED) how many units of the step hold elements of the reduction.
 struct Source {
     u32x4_t rs;
     uint32_t soff;
     int units;
 };
+// base: the half's first row (RED) or column; rows, cols: how many of them exist, which may be none.
 template <typename T, bool RED>
-__device__ __forceinline__ Source step_source(const void* base, long long ld, int rows, int cols, int red, int red_rows, int kt) {
+__device__ __forceinline__ Source step_source(const void* base, long long ld, int rows, int cols, int red, int red_rows, int kt,
+                                              bool any) {
     constexpr int kEs = sizeof(T), kStep = 128 / kEs, kEpu = 16 / kEs;
     Source s;
     const char* p = static_cast<const char*>(base);
     if constexpr (RED) {
-        s.rs = make_rsrc(p, static_cast<uint32_t>(((rows - 1) * ld + red) * kEs));
+        s.rs = make_rsrc(p, any && rows > 0 ? static_cast<uint32_t>(((rows - 1) * ld + red) * kEs) : 0);
         s.soff = kt * 128;
         s.units = (red - kt * kStep + kEpu - 1) / kEpu;
     } else {
         const int left = min(kStep, red_rows - kt * kStep), width = (cols + kEpu - 1) / kEpu * kEpu;
-        s.rs = make_rsrc(p + static_cast<long long>(kt) * kStep * ld * kEs, static_cast<uint32_t>(((left - 1) * ld + width) * kEs));
+        s.rs = make_rsrc(p + static_cast<long long>(kt) * kStep * ld * kEs,
+                         any && cols > 0 ? static_cast<uint32_t>(((left - 1) * ld + width) * kEs) : 0);
         s.soff = 0;
         s.units = 8;
     }
@@ -235,12 +236,14 @@ __device__ __forceinline__ int round8(int n) { return (n + 7) & ~7; }
 // ---- the product ----------------------------------------------------------------------------------
 template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int KIND>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void proj_kernel(const ProjArgs p) {
-    constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
-    static_assert(TN == 4 && TM <= 8, "a wave's tile is up to 128 x 64");
-    constexpr bool PAIRS = KIND == kProjGated;
-    typedef Side<T, AR, BM, NW> A;
-    typedef Side<T, BR, BN, NW> B;
-    constexpr int kStage = A::kBytes + B::kBytes, kEs = sizeof(T), kStep = 128 / kEs;
+    constexpr int NW = WM * WN, TI = BM / 2 / WM / 16, TJ = BN / 2 / WN / 16;   // blocks of a wave in a half
+    static_assert(TJ == 2 && TI <= 4, "a wave's tile is up to 128 x 64");
+    constexpr bool PAIRS = KIND == kProjGated;       // B's halves: the two projections
+    typedef Half<T, AR, BM / 2, NW> A;
+    typedef Half<T, BR, BN / 2, NW> B;
+    // LDS of a stage: A's upper and lower, B's left and right half
+    constexpr int kStage = 2 * (A::kBytes + B::kBytes), kAb = A::kBytes, kBl = 2 * A::kBytes, kBr = kBl + B::kBytes;
+    constexpr int kEs = sizeof(T), kStep = 128 / kEs;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -267,163 +270,189 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 
     A sa;
     B sb;
-    sa.template init<false>(wave, lane, wm * TM, g.lda);
-    sb.template init<PAIRS>(wave, lane, wn * TN, g.ldb);
+    sa.init(wave, lane, wm * TI, g.lda);
+    sb.init(wave, lane, wn * TJ, g.ldb);
 
     const int nk1 = (p.red + kStep - 1) / kStep;
     const int s0 = split * p.per_split, s1 = min(s0 + p.per_split, nk1 * p.phases);
-    const int arows = min(BM, g.M - m0), bcols = min(kCols, g.bn - n0);
+    // the second halves lie `a_next`, `b_next` bytes on (pairs: in the other projection)
     const size_t aoff = static_cast<size_t>(m0) * (AR ? g.lda : 1), boff = static_cast<size_t>(n0) * (BR ? g.ldb : 1);
-    auto a_src = [&](int kt) {
-        const bool second = kt >= nk1;
-        return step_source<T, AR>(static_cast<const T*>(second ? g.a2 : g.a) + aoff, g.lda, arows, g.M - m0, p.red,
-                                  p.red_rows, second ? kt - nk1 : kt);
+    const size_t a_half = static_cast<size_t>(BM / 2) * (AR ? g.lda : 1);
+    const size_t b_half = PAIRS ? 0 : static_cast<size_t>(BN / 2) * (BR ? g.ldb : 1);
+    auto a_src = [&](int kt, int h) {
+        const bool second = kt >= nk1, any = kt < s1;
+        const int left = g.M - m0 - h * (BM / 2);
+        return step_source<T, AR>(static_cast<const T*>(second ? g.a2 : g.a) + aoff + h * a_half, g.lda, min(BM / 2, left), left,
+                                  p.red, p.red_rows, second ? kt - nk1 : kt, any);
     };
-    auto b_src = [&](int kt) {
-        // (pairs: a wave's copies all belong to one of the two projections)
-        const bool second = PAIRS ? ((wave >> 1) & 1) != 0 : kt >= nk1;
-        return step_source<T, BR>(static_cast<const T*>(second ? g.b2 : g.b) + boff, g.ldb, bcols, g.bn - n0, p.red,
-                                  p.red_rows, !PAIRS && second ? kt - nk1 : kt);
+    auto b_src = [&](int kt, int h) {
+        const bool second = PAIRS ? h == 1 : kt >= nk1, any = kt < s1;
+        const int left = g.bn - n0 - (PAIRS ? 0 : h * (BN / 2));
+        return step_source<T, BR>(static_cast<const T*>(second ? g.b2 : g.b) + boff + h * b_half, g.ldb, min(BN / 2, left), left,
+                                  p.red, p.red_rows, !PAIRS && second ? kt - nk1 : kt, any);
     };
     const uint32_t lds0 = lds_addr_of(smem);
-    auto copy_a = [&](const Source& s, int i, uint32_t at) {
-        const uint32_t o = AR && sa.unit >= s.units ? kOutside : sa.off[i];
+    auto copy = [&](const auto& side, bool red, const Source& s, int i, uint32_t at) {
+        const uint32_t o = red && side.unit >= s.units ? kOutside : side.off[i];
         buf2lds16(s.rs, o, s.soff, at + (wave + NW * i) * 1024);
     };
-    auto copy_b = [&](const Source& s, int i, uint32_t at) {
-        const uint32_t o = BR && sb.unit >= s.units ? kOutside : sb.off[i];
-        buf2lds16(s.rs, o, s.soff, at + A::kBytes + (wave + NW * i) * 1024);
-    };
+    // copies of one half each: h = 0, 1 of A, of B
+    auto copy_a = [&](const Source& s, int h, int i, uint32_t st) { copy(sa, AR, s, i, st + h * kAb); };
+    auto copy_b = [&](const Source& s, int h, int i, uint32_t st) { copy(sb, BR, s, i, st + (h ? kBr : kBl)); };
 
-    f32x4_t acc[TM][TN];
+    f32x4_t acc[2][TI][2][TJ];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) acc[x][i][y][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
     if (s0 < s1) {
-        constexpr int kCopies = A::kCopies + B::kCopies;
-        {
-            const Source ssa = a_src(s0), ssb = b_src(s0);
+        constexpr int kCA = A::kCopies, kCB = B::kCopies, kPair = kCA + kCB;
+        // what one pair of quarters fetches: A's upper and B's left half, or B's right and A's lower
+        auto fetch = [&](int kt, int pair, uint32_t st) {
+            const Source x = a_src(kt, pair), y = b_src(kt, pair);
 #pragma unroll
-            for (int i = 0; i < A::kCopies; ++i) copy_a(ssa, i, lds0);
+            for (int i = 0; i < kCA; ++i) copy_a(x, pair, i, st);
 #pragma unroll
-            for (int i = 0; i < B::kCopies; ++i) copy_b(ssb, i, lds0);
-        }
-        if (s0 + 1 < s1) {
-            const Source ssa = a_src(s0 + 1), ssb = b_src(s0 + 1);
+            for (int i = 0; i < kCB; ++i) copy_b(y, pair, i, st);
+        };
+        fetch(s0, 0, lds0);
+        fetch(s0, 1, lds0);
+        fetch(s0 + 1, 0, lds0 + kStage);
+        fetch(s0 + 1, 1, lds0 + kStage);
+        wait_vmcnt<2 * kPair>();
+        lds_barrier();
+        u16x8_t fa[2][TI][2], fb[2][TJ][2];          // A: upper, lower; B: by turns left and right
 #pragma unroll
-            for (int i = 0; i < A::kCopies; ++i) copy_a(ssa, i, lds0 + kStage);
+        for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
-            for (int i = 0; i < B::kCopies; ++i) copy_b(ssb, i, lds0 + kStage);
-            wait_vmcnt<kCopies>();
-        } else {
-            wait_vmcnt<0>();
+            for (int i = 0; i < TI; ++i) fa[0][i][ks] = sa.read(lds0, i, ks);
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) fb[0][j][ks] = sb.read(lds0 + kBl, j, ks);
         }
         lds_barrier();
-        u16x8_t fa[2][TM], fb[2][TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) fb[0][j] = sb.read(lds0 + A::kBytes, j, 0);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) fa[0][i] = sa.read(lds0, i, 0);
         uint32_t cur = lds0, oth = lds0 + kStage;
-        for (int kt = s0; kt < s1; ++kt) {
-            // first half's products; the second half's fragments come in
+        // A quarter: its products, between them the reads of the half that comes in (from `in`:
+        // A's lower (1) or upper (0) half, or B's right (1) or left (0)) and copies.
+        auto quarter = [&](auto x, auto y, auto bx, auto read_a, auto half_in, uint32_t in, auto&& copies) {
+            constexpr int X = x(), Y = y(), BX = bx(), RA = read_a(), H = half_in();
+            constexpr int kReads = RA ? 2 * TI : 2 * TJ;
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                if (i == 0) {
+            for (int i = 0; i < TI; ++i) {
+                constexpr int kEach = (kReads + TI - 1) / TI;
 #pragma unroll
-                    for (int j = 0; j < TN; ++j) fb[1][j] = sb.read(cur + A::kBytes, j, 1);
+                for (int r = i * kEach; r < (i + 1) * kEach && r < kReads; ++r) {
+                    if constexpr (RA)
+                        fa[H][r >> 1][r & 1] = sa.read(in, r >> 1, r & 1);
+                    else
+                        fb[H][r >> 1][r & 1] = sb.read(in, r >> 1, r & 1);
                 }
-                fa[1][i] = sa.read(cur, i, 1);
+                copies(i);
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = frag_mul<T>(fb[0][j], fa[0][i], acc[i][j]);
+                for (int j = 0; j < TJ; ++j)
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) acc[X][i][Y][j] = frag_mul<T>(fb[BX][j][ks], fa[X][i][ks], acc[X][i][Y][j]);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            wait_vmcnt<0>();     // the next step has landed for this wave,
-            lds_barrier();       // and for all; all have read this step
-            const bool more = kt + 2 < s1, next = kt + 1 < s1;
-            Source ssa{}, ssb{};
-            if (more) {
-                ssa = a_src(kt + 2);
-                ssb = b_src(kt + 2);
-            }
-            // second half's products; the next step's first fragments, the copies of the one after
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                constexpr int kPer = (kCopies + TM - 1) / TM;
-                if (more) {
-#pragma unroll
-                    for (int c = i * kPer; c < (i + 1) * kPer && c < kCopies; ++c) {
-                        if (c < A::kCopies)
-                            copy_a(ssa, c, cur);
-                        else
-                            copy_b(ssb, c - A::kCopies, cur);
-                    }
-                }
-                if (next) {
-                    if (i == 0) {
-#pragma unroll
-                        for (int j = 0; j < TN; ++j) fb[0][j] = sb.read(oth + A::kBytes, j, 0);
-                    }
-                    fa[0][i] = sa.read(oth, i, 0);
-                }
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = frag_mul<T>(fb[1][j], fa[1][i], acc[i][j]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        };
+        constexpr std::integral_constant<int, 0> c0{};
+        constexpr std::integral_constant<int, 1> c1{};
+        // A step whose left half of B is in fb[P]; the next step's comes into the other.
+        auto step = [&](int kt, auto par) {
+            constexpr int P = par();
+            constexpr std::integral_constant<int, P> l{};
+            constexpr std::integral_constant<int, P ^ 1> r{};
+            Source x = a_src(kt + 2, 0), y = b_src(kt + 2, 0);
+            quarter(c0, c0, l, c0, r, cur + kBr, [&](int i) {
+                if (i < kCA) copy_a(x, 0, i, cur);
+            });
+            quarter(c0, c1, r, c1, c1, cur + kAb, [&](int i) {
+                if (i < kCB) copy_b(y, 0, i, cur);
+            });
+            wait_vmcnt<2 * kPair>();   // the next step's upper and left halves have landed for this wave,
+            lds_barrier();             // and for all; all have read this step's lower and right ones
+            x = a_src(kt + 2, 1);
+            y = b_src(kt + 2, 1);
+            quarter(c1, c1, r, c1, c0, oth, [&](int i) {
+                if (i < kCA) copy_a(x, 1, i, cur);
+            });
+            quarter(c1, c0, l, c0, r, oth + kBl, [&](int i) {
+                if (i < kCB) copy_b(y, 1, i, cur);
+            });
+            wait_vmcnt<2 * kPair>();   // likewise, the other halves
+            lds_barrier();
             const uint32_t s = cur;
             cur = oth;
             oth = s;
+        };
+        int kt = s0;
+        for (; kt + 1 < s1; kt += 2) {
+            step(kt, c0);
+            step(kt + 1, c1);
         }
+        if (kt < s1) step(kt, c0);
+        wait_vmcnt<0>();               // (the empty copies past the end, before LDS has other uses)
     }
     __syncthreads();   // the stages become the waves' turning places
 
     // The sums of 16 rows at a time go through LDS, so that a lane holds eight adjacent columns
-    // of a row and eight lanes a row's 64: whole lines to load and store.
+    // of a row: the wave's 32 columns of the left half, then of the right.
     constexpr int kPitch = 64 + 4;
     float* const turn = reinterpret_cast<float*>(smem) + wave * 16 * kPitch;
     const int np = round8(g.N);
     constexpr int kPass = PAIRS ? 1 : 2;
+    auto put = [&](auto half) {
+        constexpr int x = half();
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+        for (int i = 0; i < TI; ++i) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4_t*>(turn + l16 * kPitch + 16 * j + 4 * g4) = acc[i][j];
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int q = 0; q < kPass; ++q) {
-            const int row = PAIRS ? lane >> 2 : q * 8 + (lane >> 3);
-            const int u = PAIRS ? lane & 3 : lane & 7;
-            const float* src = turn + row * kPitch + (PAIRS ? (u >> 1) * 32 + (u & 1) * 8 : u * 8);
-            float v[8], w[8];
+                for (int j = 0; j < TJ; ++j)
+                    *reinterpret_cast<f32x4_t*>(turn + l16 * kPitch + 32 * y + 16 * j + 4 * g4) = acc[x][i][y][j];
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const f32x4_t x = *reinterpret_cast<const f32x4_t*>(src + 4 * k);
-                f32x4_t y{};
-                if (PAIRS) y = *reinterpret_cast<const f32x4_t*>(src + 16 + 4 * k);
+            for (int q = 0; q < kPass; ++q) {
+                const int row = PAIRS ? lane >> 2 : q * 8 + (lane >> 3);
+                const int u = PAIRS ? lane & 3 : lane & 7;
+                const float* src = turn + row * kPitch + u * 8;
+                float v[8], w[8];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    v[4 * k + r] = x[r];
-                    w[4 * k + r] = y[r];
+                for (int k = 0; k < 2; ++k) {
+                    const f32x4_t e = *reinterpret_cast<const f32x4_t*>(src + 4 * k);
+                    f32x4_t f{};
+                    if (PAIRS) f = *reinterpret_cast<const f32x4_t*>(src + 32 + 4 * k);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        v[4 * k + r] = e[r];
+                        w[4 * k + r] = f[r];
+                    }
+                }
+                const int m = m0 + x * (BM / 2) + (wm * TI + i) * 16 + row;
+                const int n = n0 + (u >> 2) * (BN / 2) + wn * 32 + (u & 3) * 8;
+                if (m >= g.M || n >= g.N) continue;
+                if (p.splits > 1) {
+                    const size_t plane = static_cast<size_t>(g.M) * np;
+                    float* o = p.part + g.part + split * plane * (PAIRS ? 2 : 1) + static_cast<size_t>(m) * np + n;
+                    store8<float>(o, v, 8);
+                    if (PAIRS) store8<float>(o + plane, w, 8);
+                } else {
+                    finish8<T, KIND>(p.e, g, m, n, v, w);
                 }
             }
-            const int m = m0 + (wm * TM + i) * 16 + row, n = n0 + wn * (PAIRS ? 32 : 64) + u * 8;
-            if (m >= g.M || n >= g.N) continue;
-            if (p.splits > 1) {
-                const size_t plane = static_cast<size_t>(g.M) * np;
-                float* o = p.part + g.part + split * plane * (PAIRS ? 2 : 1) + static_cast<size_t>(m) * np + n;
-                store8<float>(o, v, 8);
-                if (PAIRS) store8<float>(o + plane, w, 8);
-            } else {
-                finish8<T, KIND>(p.e, g, m, n, v, w);
-            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    }
+    };
+    put(std::integral_constant<int, 0>());
+    put(std::integral_constant<int, 1>());
 }
 
 // Sums of split reductions, in the order of the splits.
