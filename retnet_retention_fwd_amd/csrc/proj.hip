@@ -128,26 +128,53 @@ struct Source {
     uint32_t soff;
     int units;
 };
-// base: the half's first row (RED) or column; rows, cols: how many of them exist, which may be none.
-template <typename T, bool RED>
-__device__ __forceinline__ Source step_source(const void* base, long long ld, int rows, int cols, int red, int red_rows, int kt,
-                                              bool any) {
-    constexpr int kEs = sizeof(T), kStep = 128 / kEs, kEpu = 16 / kEs;
-    Source s;
-    const char* p = static_cast<const char*>(base);
-    if constexpr (RED) {
-        s.rs = make_rsrc(p, any && rows > 0 ? static_cast<uint32_t>(((rows - 1) * ld + red) * kEs) : 0);
-        s.soff = kt * 128;
-        s.units = (red - kt * kStep + kEpu - 1) / kEpu;
-    } else {
-        const int left = min(kStep, red_rows - kt * kStep), width = (cols + kEpu - 1) / kEpu * kEpu;
-        s.rs = make_rsrc(p + static_cast<long long>(kt) * kStep * ld * kEs,
-                         any && cols > 0 ? static_cast<uint32_t>(((left - 1) * ld + width) * kEs) : 0);
-        s.soff = 0;
-        s.units = 8;
-    }
-    return s;
+// A value that the compiler keeps in scalar registers instead of loading it again.
+template <typename V>
+__device__ __forceinline__ V held(V v) {
+    asm volatile("" : "+s"(v));
+    return v;
 }
+// An operand of this tile: the addresses of its first half's rows (RED) or columns in both
+// phases, the way to the second half, and how much of a half there is (none past the edge).
+template <typename T, bool RED, int R>
+struct Operand {
+    static constexpr int kEs = sizeof(T), kStep = 128 / kEs, kEpu = 16 / kEs;
+    uint64_t first, second, half;
+    int ld;
+    uint32_t size[2];          // RED: bytes of the resource; else: of a row's end
+
+    __device__ __forceinline__ void init(const void* a, const void* b, int ld_, int at, int count, int red) {
+        ld = held(ld_);
+        const uint64_t o = static_cast<uint64_t>(at) * (RED ? ld : 1) * kEs;
+        first = held(reinterpret_cast<uint64_t>(a) + o);
+        second = held(reinterpret_cast<uint64_t>(b) + o);
+        half = held(static_cast<uint64_t>(R) * (RED ? ld : 1) * kEs);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int left = count - at - h * R;
+            uint32_t n = 0;
+            if (left > 0) n = static_cast<uint32_t>(RED ? (min(R, left) - 1) * static_cast<long long>(ld) + red : (left + kEpu - 1) / kEpu * kEpu) * kEs;
+            size[h] = held(n);
+        }
+    }
+    // Half h of step kt of the phase that `two` names; any: there is such a step.
+    __device__ __forceinline__ Source step(int kt, bool two, int h, int red, int red_rows, bool any) const {
+        Source s;
+        uint64_t p = (two ? second : first) + (h ? half : 0);
+        uint32_t n = size[h];
+        if constexpr (RED) {
+            s.soff = kt * 128;
+            s.units = (red - kt * kStep + kEpu - 1) / kEpu;
+        } else {
+            p += static_cast<uint64_t>(kt) * (static_cast<uint64_t>(kStep * kEs) * ld);
+            if (n != 0) n += (min(kStep, red_rows - kt * kStep) - 1) * ld * kEs;
+            s.soff = 0;
+            s.units = 8;
+        }
+        s.rs = u32x4_t{static_cast<uint32_t>(p), static_cast<uint32_t>(p >> 32) & 0xFFFFu, any ? n : 0, 0x00020000u};
+        return s;
+    }
+};
 
 // ---- what happens to the sums -------------------------------------------------------------------
 template <typename T>
@@ -275,21 +302,22 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 
     const int nk1 = (p.red + kStep - 1) / kStep;
     const int s0 = split * p.per_split, s1 = min(s0 + p.per_split, nk1 * p.phases);
-    // the second halves lie `a_next`, `b_next` bytes on (pairs: in the other projection)
-    const size_t aoff = static_cast<size_t>(m0) * (AR ? g.lda : 1), boff = static_cast<size_t>(n0) * (BR ? g.ldb : 1);
-    const size_t a_half = static_cast<size_t>(BM / 2) * (AR ? g.lda : 1);
-    const size_t b_half = PAIRS ? 0 : static_cast<size_t>(BN / 2) * (BR ? g.ldb : 1);
+    Operand<T, AR, BM / 2> oa;
+    Operand<T, BR, BN / 2> ob;       // pairs: the halves are the two projections, at the same columns
+    oa.init(g.a, p.phases > 1 ? g.a2 : g.a, g.lda, m0, g.M, p.red);
+    ob.init(g.b, PAIRS || p.phases > 1 ? g.b2 : g.b, g.ldb, n0, g.bn, p.red);
+    if (PAIRS) {
+        ob.half = held(ob.second - ob.first);
+        ob.size[1] = ob.size[0];
+    }
+    const int red = held(p.red), red_rows = held(p.red_rows);
     auto a_src = [&](int kt, int h) {
-        const bool second = kt >= nk1, any = kt < s1;
-        const int left = g.M - m0 - h * (BM / 2);
-        return step_source<T, AR>(static_cast<const T*>(second ? g.a2 : g.a) + aoff + h * a_half, g.lda, min(BM / 2, left), left,
-                                  p.red, p.red_rows, second ? kt - nk1 : kt, any);
+        const bool two = kt >= nk1;
+        return oa.step(two ? kt - nk1 : kt, two, h, red, red_rows, kt < s1);
     };
     auto b_src = [&](int kt, int h) {
-        const bool second = PAIRS ? h == 1 : kt >= nk1, any = kt < s1;
-        const int left = g.bn - n0 - (PAIRS ? 0 : h * (BN / 2));
-        return step_source<T, BR>(static_cast<const T*>(second ? g.b2 : g.b) + boff + h * b_half, g.ldb, min(BN / 2, left), left,
-                                  p.red, p.red_rows, !PAIRS && second ? kt - nk1 : kt, any);
+        const bool two = !PAIRS && kt >= nk1;
+        return ob.step(two ? kt - nk1 : kt, two, h, red, red_rows, kt < s1);
     };
     const uint32_t lds0 = lds_addr_of(smem);
     auto copy = [&](const auto& side, bool red, const Source& s, int i, uint32_t at) {
