@@ -261,10 +261,10 @@ __device__ __forceinline__ void finish8(const ProjEpi& e, const ProjGroup& g, in
 __device__ __forceinline__ int round8(int n) { return (n + 7) & ~7; }
 
 // ---- the product ----------------------------------------------------------------------------------
-template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int KIND>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void proj_kernel(const ProjArgs p) {
+template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int WAVES, int KIND>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WAVES, WAVES))) void proj_kernel(const ProjArgs p) {
     constexpr int NW = WM * WN, TI = BM / 2 / WM / 16, TJ = BN / 2 / WN / 16;   // blocks of a wave in a half
-    static_assert(TJ == 2 && TI <= 4, "a wave's tile is up to 128 x 64");
+    static_assert((TJ == 2 || TJ == 4) && TI <= 4, "a wave's tile is up to 128 x 128");
     constexpr bool PAIRS = KIND == kProjGated;       // B's halves: the two projections
     typedef Half<T, AR, BM / 2, NW> A;
     typedef Half<T, BR, BN / 2, NW> B;
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
             constexpr int kReads = RA ? 2 * TI : 2 * TJ;
 #pragma unroll
             for (int i = 0; i < TI; ++i) {
-                constexpr int kEach = (kReads + TI - 1) / TI;
+                constexpr int kEach = (kReads + TI / 2 - 1) / (TI / 2);
 #pragma unroll
                 for (int r = i * kEach; r < (i + 1) * kEach && r < kReads; ++r) {
                     if constexpr (RA)
@@ -396,20 +396,20 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
             constexpr std::integral_constant<int, P ^ 1> r{};
             Source x = a_src(kt + 2, 0), y = b_src(kt + 2, 0);
             quarter(c0, c0, l, c0, r, cur + kBr, [&](int i) {
-                if (i < kCA) copy_a(x, 0, i, cur);
+                if (i >= TI - kCA) copy_a(x, 0, i - TI + kCA, cur);
             });
             quarter(c0, c1, r, c1, c1, cur + kAb, [&](int i) {
-                if (i < kCB) copy_b(y, 0, i, cur);
+                if (i >= TI - kCB) copy_b(y, 0, i - TI + kCB, cur);
             });
             wait_vmcnt<2 * kPair>();   // the next step's upper and left halves have landed for this wave,
             lds_barrier();             // and for all; all have read this step's lower and right ones
             x = a_src(kt + 2, 1);
             y = b_src(kt + 2, 1);
             quarter(c1, c1, r, c1, c0, oth, [&](int i) {
-                if (i < kCA) copy_a(x, 1, i, cur);
+                if (i >= TI - kCA) copy_a(x, 1, i - TI + kCA, cur);
             });
             quarter(c1, c0, l, c0, r, oth + kBl, [&](int i) {
-                if (i < kCB) copy_b(y, 1, i, cur);
+                if (i >= TI - kCB) copy_b(y, 1, i - TI + kCB, cur);
             });
             wait_vmcnt<2 * kPair>();   // likewise, the other halves
             lds_barrier();
@@ -428,11 +428,11 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     __syncthreads();   // the stages become the waves' turning places
 
     // The sums of 16 rows at a time go through LDS, so that a lane holds eight adjacent columns
-    // of a row: the wave's 32 columns of the left half, then of the right.
-    constexpr int kPitch = 64 + 4;
+    // of a row: the wave's columns of the left half, then of the right.
+    constexpr int kWide = TJ * 16, kPitch = 2 * kWide + 4;
+    constexpr int kUnits = (PAIRS ? 1 : 2) * kWide / 8, kRows = 64 / kUnits;
     float* const turn = reinterpret_cast<float*>(smem) + wave * 16 * kPitch;
     const int np = round8(g.N);
-    constexpr int kPass = PAIRS ? 1 : 2;
     auto put = [&](auto half) {
         constexpr int x = half();
 #pragma unroll
@@ -441,21 +441,20 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
             for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int j = 0; j < TJ; ++j)
-                    *reinterpret_cast<f32x4_t*>(turn + l16 * kPitch + 32 * y + 16 * j + 4 * g4) = acc[x][i][y][j];
+                    *reinterpret_cast<f32x4_t*>(turn + l16 * kPitch + kWide * y + 16 * j + 4 * g4) = acc[x][i][y][j];
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-            for (int q = 0; q < kPass; ++q) {
-                const int row = PAIRS ? lane >> 2 : q * 8 + (lane >> 3);
-                const int u = PAIRS ? lane & 3 : lane & 7;
+#pragma unroll 1
+            for (int q = 0; q < 16 / kRows; ++q) {
+                const int row = q * kRows + lane / kUnits, u = lane % kUnits;
                 const float* src = turn + row * kPitch + u * 8;
                 float v[8], w[8];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const f32x4_t e = *reinterpret_cast<const f32x4_t*>(src + 4 * k);
                     f32x4_t f{};
-                    if (PAIRS) f = *reinterpret_cast<const f32x4_t*>(src + 32 + 4 * k);
+                    if (PAIRS) f = *reinterpret_cast<const f32x4_t*>(src + kWide + 4 * k);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         v[4 * k + r] = e[r];
@@ -463,7 +462,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
                     }
                 }
                 const int m = m0 + x * (BM / 2) + (wm * TI + i) * 16 + row;
-                const int n = n0 + (u >> 2) * (BN / 2) + wn * 32 + (u & 3) * 8;
+                const int n = n0 + u / (kWide / 8) * (BN / 2) + wn * kWide + u % (kWide / 8) * 8;
                 if (m >= g.M || n >= g.N) continue;
                 if (p.splits > 1) {
                     const size_t plane = static_cast<size_t>(g.M) * np;
@@ -568,17 +567,17 @@ int plan(ProjArgs& a, ProjKind kind, bool bf16) {
     return best;
 }
 
-template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int KIND>
+template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int WAVES, int KIND>
 hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
     constexpr int lds = 2 * (BM + BN) * 128;
     static std::once_flag attr_once;   // thread-safe one-time init of the LDS limit
     std::call_once(attr_once, [] {
-        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&proj_kernel<T, AR, BR, BM, BN, WM, WN, KIND>),
+        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&proj_kernel<T, AR, BR, BM, BN, WM, WN, WAVES, KIND>),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     });
     {
         ProfScope prof(kProfProj, st);
-        hipLaunchKernelGGL((proj_kernel<T, AR, BR, BM, BN, WM, WN, KIND>), dim3(a.tiles * a.splits), dim3(64 * WM * WN), lds,
+        hipLaunchKernelGGL((proj_kernel<T, AR, BR, BM, BN, WM, WN, WAVES, KIND>), dim3(a.tiles * a.splits), dim3(64 * WM * WN), lds,
                            st, a);
     }
     hipError_t e = hipGetLastError();
@@ -593,8 +592,8 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
 
 template <typename T, bool AR, bool BR, int KIND>
 hipError_t launch_sized(const ProjArgs& a, int tile, hipStream_t st) {
-    return tile == 0 ? launch_tile<T, AR, BR, 256, 256, 2, 4, KIND>(a, st)
-                     : launch_tile<T, AR, BR, 128, 128, 2, 2, KIND>(a, st);
+    return tile == 0 ? launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st)
+                     : launch_tile<T, AR, BR, 128, 128, 2, 2, 2, KIND>(a, st);
 }
 
 template <typename T>
