@@ -369,21 +369,21 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
         auto quarter = [&](auto x, auto y, auto bx, auto read_a, auto half_in, uint32_t in, auto&& copies) {
             constexpr int X = x(), Y = y(), BX = bx(), RA = read_a(), H = half_in();
             constexpr int kReads = RA ? 2 * TI : 2 * TJ;
+            // Two row blocks at a time: a sum's next product comes four instructions after its last.
+            // One read or copy goes out behind each product, while the matrix cores work on it.
+            constexpr int kMul = 2 * TI * TJ;
 #pragma unroll
-            for (int i = 0; i < TI; ++i) {
-                constexpr int kEach = (kReads + TI / 2 - 1) / (TI / 2);
-#pragma unroll
-                for (int r = i * kEach; r < (i + 1) * kEach && r < kReads; ++r) {
+            for (int n = 0; n < kMul; ++n) {
+                const int j = n % TJ, e = n / TJ % 2, ks = n / (2 * TJ) % 2, i = n / (4 * TJ) * 2 + e;
+                acc[X][i][Y][j] = frag_mul<T>(fb[BX][j][ks], fa[X][i][ks], acc[X][i][Y][j]);
+                if (n < kReads) {
                     if constexpr (RA)
-                        fa[H][r >> 1][r & 1] = sa.read(in, r >> 1, r & 1);
+                        fa[H][n >> 1][n & 1] = sa.read(in, n >> 1, n & 1);
                     else
-                        fb[H][r >> 1][r & 1] = sb.read(in, r >> 1, r & 1);
+                        fb[H][n >> 1][n & 1] = sb.read(in, n >> 1, n & 1);
+                } else if ((n - kReads) % 2 == 0) {
+                    copies((n - kReads) / 2);
                 }
-                copies(i);
-#pragma unroll
-                for (int j = 0; j < TJ; ++j)
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks) acc[X][i][Y][j] = frag_mul<T>(fb[BX][j][ks], fa[X][i][ks], acc[X][i][Y][j]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -396,20 +396,20 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
             constexpr std::integral_constant<int, P ^ 1> r{};
             Source x = a_src(kt + 2, 0), y = b_src(kt + 2, 0);
             quarter(c0, c0, l, c0, r, cur + kBr, [&](int i) {
-                if (i >= TI - kCA) copy_a(x, 0, i - TI + kCA, cur);
+                if (i < kCA) copy_a(x, 0, i, cur);
             });
             quarter(c0, c1, r, c1, c1, cur + kAb, [&](int i) {
-                if (i >= TI - kCB) copy_b(y, 0, i - TI + kCB, cur);
+                if (i < kCB) copy_b(y, 0, i, cur);
             });
             wait_vmcnt<2 * kPair>();   // the next step's upper and left halves have landed for this wave,
             lds_barrier();             // and for all; all have read this step's lower and right ones
             x = a_src(kt + 2, 1);
             y = b_src(kt + 2, 1);
             quarter(c1, c1, r, c1, c0, oth, [&](int i) {
-                if (i >= TI - kCA) copy_a(x, 1, i - TI + kCA, cur);
+                if (i < kCA) copy_a(x, 1, i, cur);
             });
             quarter(c1, c0, l, c0, r, oth + kBl, [&](int i) {
-                if (i >= TI - kCB) copy_b(y, 1, i - TI + kCB, cur);
+                if (i < kCB) copy_b(y, 1, i, cur);
             });
             wait_vmcnt<2 * kPair>();   // likewise, the other halves
             lds_barrier();
