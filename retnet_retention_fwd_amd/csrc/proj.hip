@@ -41,9 +41,13 @@ typedef float f32x4u_t __attribute__((ext_vector_type(4)));
 // Lane (g, l) = (lane / 16, lane % 16) brings row l of a and column l of b, 16 bytes of the
 // reduction from 16 g on, and holds columns ... of c as the matrix instructions do; which
 // elements meet in one instruction is the same for both operands, so any order will do.
-template <typename T>
+template <typename T, bool FIXED>
 __device__ __forceinline__ f32x4_t frag_mul(u16x8_t a, u16x8_t b, f32x4_t c) {
-    if constexpr (sizeof(T) == 2) {
+    if constexpr (FIXED) {
+        static_assert(sizeof(T) == 2, "bf16");
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+        return c;
+    } else if constexpr (sizeof(T) == 2) {
         return mfma16(a, b, c);
     } else {
         const f32x4_t x = __builtin_bit_cast(f32x4_t, a), y = __builtin_bit_cast(f32x4_t, b);
@@ -121,27 +125,24 @@ struct Half {
     }
 };
 
-// Where a step's copies of a half come from: the resource (empty past the last step: zeros
-// arrive), its scalar offset, and (RED) how many units of the step hold elements of the reduction.
-struct Source {
-    u32x4_t rs;
-    uint32_t soff;
-    int units;
-};
 // A value that the compiler keeps in scalar registers instead of loading it again.
 template <typename V>
 __device__ __forceinline__ V held(V v) {
     asm volatile("" : "+s"(v));
     return v;
 }
-// An operand of this tile: the addresses of its first half's rows (RED) or columns in both
-// phases, the way to the second half, and how much of a half there is (none past the edge).
+// Where the copies of an operand's two halves come from, step after step: a resource each (empty
+// where there is nothing: zeros arrive), the scalar offset, and (RED) how many of a row's units
+// from here on hold elements of the reduction.
 template <typename T, bool RED, int R>
 struct Operand {
     static constexpr int kEs = sizeof(T), kStep = 128 / kEs, kEpu = 16 / kEs;
-    uint64_t first, second, half;
+    uint64_t first, second, half;   // address of the tile in both phases, way to the second half
     int ld;
-    uint32_t size[2];          // RED: bytes of the resource; else: of a row's end
+    uint32_t size[2];               // RED: bytes of a half; else: of its last row
+    u32x4_t rs[2];
+    uint32_t soff;
+    int units;
 
     __device__ __forceinline__ void init(const void* a, const void* b, int ld_, int at, int count, int red) {
         ld = held(ld_);
@@ -157,22 +158,34 @@ struct Operand {
             size[h] = held(n);
         }
     }
-    // Half h of step kt of the phase that `two` names; any: there is such a step.
-    __device__ __forceinline__ Source step(int kt, bool two, int h, int red, int red_rows, bool any) const {
-        Source s;
-        uint64_t p = (two ? second : first) + (h ? half : 0);
-        uint32_t n = size[h];
-        if constexpr (RED) {
-            s.soff = kt * 128;
-            s.units = (red - kt * kStep + kEpu - 1) / kEpu;
-        } else {
-            p += static_cast<uint64_t>(kt) * (static_cast<uint64_t>(kStep * kEs) * ld);
-            if (n != 0) n += (min(kStep, red_rows - kt * kStep) - 1) * ld * kEs;
-            s.soff = 0;
-            s.units = 8;
+    // To step kt of the phase that `two` names; any: there is such a step.
+    __device__ __forceinline__ void go(int kt, bool two, int red, int red_rows, bool any) {
+        soff = RED ? kt * 128 : 0;
+        units = RED ? (red - kt * kStep + kEpu - 1) / kEpu : 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint64_t p = (two ? second : first) + (h ? half : 0);
+            uint32_t n = size[h];
+            if constexpr (!RED) {
+                p += static_cast<uint64_t>(kt) * (static_cast<uint64_t>(kStep * kEs) * ld);
+                if (n != 0) n += (min(kStep, red_rows - kt * kStep) - 1) * ld * kEs;
+            }
+            rs[h] = u32x4_t{static_cast<uint32_t>(p), static_cast<uint32_t>(p >> 32) & 0xFFFFu, any ? n : 0, 0x00020000u};
         }
-        s.rs = u32x4_t{static_cast<uint32_t>(p), static_cast<uint32_t>(p >> 32) & 0xFFFFu, any ? n : 0, 0x00020000u};
-        return s;
+    }
+    // To the next step, where both are whole steps of one phase.
+    __device__ __forceinline__ void next() {
+        if constexpr (RED) {
+            soff += 128;
+            units -= 8;
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint64_t p = (static_cast<uint64_t>(rs[h][1]) << 32 | rs[h][0]) + static_cast<uint64_t>(kStep * kEs) * ld;
+                rs[h][0] = static_cast<uint32_t>(p);
+                rs[h][1] = static_cast<uint32_t>(p >> 32);
+            }
+        }
     }
 };
 
@@ -266,6 +279,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
     constexpr int NW = WM * WN, TI = BM / 2 / WM / 16, TJ = BN / 2 / WN / 16;   // blocks of a wave in a half
     static_assert((TJ == 2 || TJ == 4) && TI <= 4, "a wave's tile is up to 128 x 128");
     constexpr bool PAIRS = KIND == kProjGated;       // B's halves: the two projections
+    constexpr bool kFixed = WAVES == 1;
     typedef Half<T, AR, BM / 2, NW> A;
     typedef Half<T, BR, BN / 2, NW> B;
     // LDS of a stage: A's upper and lower, B's left and right half
@@ -311,22 +325,29 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
         ob.size[1] = ob.size[0];
     }
     const int red = held(p.red), red_rows = held(p.red_rows);
-    auto a_src = [&](int kt, int h) {
+    // Sources of step kt.  Steps follow each other by `next` except at the ends of a phase and of
+    // this workgroup's part: `turn` is the next such step.
+    int turn_at = 0;
+    auto source = [&](int kt) {
+        if (kt != turn_at) {
+            oa.next();
+            ob.next();
+            return;
+        }
         const bool two = kt >= nk1;
-        return oa.step(two ? kt - nk1 : kt, two, h, red, red_rows, kt < s1);
-    };
-    auto b_src = [&](int kt, int h) {
-        const bool two = !PAIRS && kt >= nk1;
-        return ob.step(two ? kt - nk1 : kt, two, h, red, red_rows, kt < s1);
+        const int k = two ? kt - nk1 : kt;
+        oa.go(k, two, red, red_rows, kt < s1);
+        ob.go(k, two && !PAIRS, red, red_rows, kt < s1);
+        turn_at = kt >= s1 ? kt + 1 : min(s1, k >= nk1 - 1 ? kt + 1 : kt + (nk1 - 1 - k));
     };
     const uint32_t lds0 = lds_addr_of(smem);
-    auto copy = [&](const auto& side, bool red, const Source& s, int i, uint32_t at) {
-        const uint32_t o = red && side.unit >= s.units ? kOutside : side.off[i];
-        buf2lds16(s.rs, o, s.soff, at + (wave + NW * i) * 1024);
+    auto copy = [&](const auto& side, const auto& from, bool red, int h, int i, uint32_t at) {
+        const uint32_t o = red && side.unit >= from.units ? kOutside : side.off[i];
+        buf2lds16(from.rs[h], o, from.soff, at + (wave + NW * i) * 1024);
     };
-    // copies of one half each: h = 0, 1 of A, of B
-    auto copy_a = [&](const Source& s, int h, int i, uint32_t st) { copy(sa, AR, s, i, st + h * kAb); };
-    auto copy_b = [&](const Source& s, int h, int i, uint32_t st) { copy(sb, BR, s, i, st + (h ? kBr : kBl)); };
+    // copy i of half h of A, of B, into the stage at `st`
+    auto copy_a = [&](int h, int i, uint32_t st) { copy(sa, oa, AR, h, i, st + h * kAb); };
+    auto copy_b = [&](int h, int i, uint32_t st) { copy(sb, ob, BR, h, i, st + (h ? kBr : kBl)); };
 
     f32x4_t acc[2][TI][2][TJ];
 #pragma unroll
@@ -340,18 +361,19 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
 
     if (s0 < s1) {
         constexpr int kCA = A::kCopies, kCB = B::kCopies, kPair = kCA + kCB;
-        // what one pair of quarters fetches: A's upper and B's left half, or B's right and A's lower
-        auto fetch = [&](int kt, int pair, uint32_t st) {
-            const Source x = a_src(kt, pair), y = b_src(kt, pair);
+        turn_at = s0;
 #pragma unroll
-            for (int i = 0; i < kCA; ++i) copy_a(x, pair, i, st);
+        for (int k = 0; k < 2; ++k) {
+            source(s0 + k);
 #pragma unroll
-            for (int i = 0; i < kCB; ++i) copy_b(y, pair, i, st);
-        };
-        fetch(s0, 0, lds0);
-        fetch(s0, 1, lds0);
-        fetch(s0 + 1, 0, lds0 + kStage);
-        fetch(s0 + 1, 1, lds0 + kStage);
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < kCA; ++i) copy_a(h, i, lds0 + k * kStage);
+#pragma unroll
+                for (int i = 0; i < kCB; ++i) copy_b(h, i, lds0 + k * kStage);
+            }
+        }
+        source(s0 + 2);
         wait_vmcnt<2 * kPair>();
         lds_barrier();
         u16x8_t fa[2][TI][2], fb[2][TJ][2];          // A: upper, lower; B: by turns left and right
@@ -371,18 +393,19 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
             constexpr int kReads = RA ? 2 * TI : 2 * TJ;
             // Two row blocks at a time: a sum's next product comes four instructions after its last.
             // One read or copy goes out behind each product, while the matrix cores work on it.
-            constexpr int kMul = 2 * TI * TJ;
+            // The copies are spread over the rest of the quarter, as the memory pipe takes 64 bytes a clock.
+            constexpr int kMul = 2 * TI * TJ, kApart = (kMul - kReads) / (kCA > kCB ? kCA : kCB);
 #pragma unroll
             for (int n = 0; n < kMul; ++n) {
                 const int j = n % TJ, e = n / TJ % 2, ks = n / (2 * TJ) % 2, i = n / (4 * TJ) * 2 + e;
-                acc[X][i][Y][j] = frag_mul<T>(fb[BX][j][ks], fa[X][i][ks], acc[X][i][Y][j]);
+                acc[X][i][Y][j] = frag_mul<T, kFixed>(fb[BX][j][ks], fa[X][i][ks], acc[X][i][Y][j]);
                 if (n < kReads) {
                     if constexpr (RA)
                         fa[H][n >> 1][n & 1] = sa.read(in, n >> 1, n & 1);
                     else
                         fb[H][n >> 1][n & 1] = sb.read(in, n >> 1, n & 1);
-                } else if ((n - kReads) % 2 == 0) {
-                    copies((n - kReads) / 2);
+                } else if ((n - kReads) % kApart == 0) {
+                    copies((n - kReads) / kApart);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -394,23 +417,21 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
             constexpr int P = par();
             constexpr std::integral_constant<int, P> l{};
             constexpr std::integral_constant<int, P ^ 1> r{};
-            Source x = a_src(kt + 2, 0), y = b_src(kt + 2, 0);
             quarter(c0, c0, l, c0, r, cur + kBr, [&](int i) {
-                if (i < kCA) copy_a(x, 0, i, cur);
+                if (i < kCA) copy_a(0, i, cur);
             });
             quarter(c0, c1, r, c1, c1, cur + kAb, [&](int i) {
-                if (i < kCB) copy_b(y, 0, i, cur);
+                if (i < kCB) copy_b(0, i, cur);
             });
             wait_vmcnt<2 * kPair>();   // the next step's upper and left halves have landed for this wave,
             lds_barrier();             // and for all; all have read this step's lower and right ones
-            x = a_src(kt + 2, 1);
-            y = b_src(kt + 2, 1);
             quarter(c1, c1, r, c1, c0, oth, [&](int i) {
-                if (i < kCA) copy_a(x, 1, i, cur);
+                if (i < kCA) copy_a(1, i, cur);
             });
             quarter(c1, c0, l, c0, r, oth + kBl, [&](int i) {
-                if (i < kCB) copy_b(y, 1, i, cur);
+                if (i < kCB) copy_b(1, i, cur);
             });
+            source(kt + 3);
             wait_vmcnt<2 * kPair>();   // likewise, the other halves
             lds_barrier();
             const uint32_t s = cur;
@@ -423,6 +444,17 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
             step(kt + 1, c1);
         }
         if (kt < s1) step(kt, c0);
+        if constexpr (kFixed) {
+            asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int i = 0; i < TI; ++i)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int j = 0; j < TJ; ++j) asm volatile("" : "+a"(acc[x][i][y][j]));
+        }
         wait_vmcnt<0>();               // (the empty copies past the end, before LDS has other uses)
     }
     __syncthreads();   // the stages become the waves' turning places
@@ -592,8 +624,12 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
 
 template <typename T, bool AR, bool BR, int KIND>
 hipError_t launch_sized(const ProjArgs& a, int tile, hipStream_t st) {
-    return tile == 0 ? launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st)
-                     : launch_tile<T, AR, BR, 128, 128, 2, 2, 2, KIND>(a, st);
+    if constexpr (sizeof(T) == 2) {
+        if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 2, 1, KIND>(a, st);
+    } else {
+        if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st);
+    }
+    return launch_tile<T, AR, BR, 128, 128, 2, 2, 2, KIND>(a, st);
 }
 
 template <typename T>
