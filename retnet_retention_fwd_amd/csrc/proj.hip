@@ -625,7 +625,7 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
 template <typename T, bool AR, bool BR, int KIND>
 hipError_t launch_sized(const ProjArgs& a, int tile, hipStream_t st) {
     if constexpr (sizeof(T) == 2) {
-        if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 2, 1, KIND>(a, st);
+        if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st);
     } else {
         if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st);
     }
