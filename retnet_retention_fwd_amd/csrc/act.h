@@ -14,56 +14,93 @@ namespace {
 // |z| cut to `most`, beyond which P is 0 or 1 in fp32; a NaN stays one.
 __device__ __forceinline__ float cut(float z, float most) { return fabsf(z) > most ? copysignf(most, z) : z; }
 
-// Normal distribution function and e^(-z^2/2).  The complementary error function of |z|/sqrt(2)
-// is Hastings' t (a1 + t (a2 + ...)) e^(-z^2/2), t = 1 / (1 + p |z|/sqrt(2)) (Abramowitz and
-// Stegun 7.1.26, off by 1.5e-7 at most, 1.3 half steps of P in fp32).
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-    const float t = rcp(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.f));
-    float p = fmaf(t, 1.061405429f, -1.453152027f);
-    p = fmaf(t, p, 1.421413741f);
-    p = fmaf(t, p, -0.284496736f);
-    p = fmaf(t, p, 0.254829592f);
-    e = __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
-    const float q = 0.5f * t * p * e;
-    return z > 0.f ? 1.f - q : q;
+// The normal distribution's weight beyond a >= 0, and e^(-a^2/2).  The complementary error function
+// of a/sqrt(2) is Hastings' t (a1 + t (a2 + ...)) e^(-a^2/2), t = 1 / (1 + p a/sqrt(2))
+// (Abramowitz and Stegun 7.1.26, off by 1.5e-7 at most: 1.3 half steps of fp32 in the half of it).
+__device__ __forceinline__ float normal_tail(float a, float& e) {
+    const float t = rcp(fmaf(a, 0.3275911f * 0.70710678118654752f, 1.f));
+    float p = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    p = fmaf(t, p, 0.5f * 1.421413741f);
+    p = fmaf(t, p, 0.5f * -0.284496736f);
+    p = fmaf(t, p, 0.5f * 0.254829592f);
+    e = __builtin_amdgcn_exp2f(a * a * (-0.5f * kLog2e));
+    return t * p * e;
 }
 // 2 sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh(./2)) / 2 is its logistic function.
 __device__ __forceinline__ float tanh_arg(float z) {
     return 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
 }
 
-__device__ __forceinline__ float act_value(float z, int act) {
-    float e;
-    switch (act) {
-        case RETN_ACT_RELU: return z <= 0.f ? 0.f : z;
-        case RETN_ACT_GELU: return z * normal_cdf(cut(z, 16.f), e);
-        case RETN_ACT_GELU_TANH: return z * sigmoid_f(tanh_arg(cut(z, 16.f)));
-        case RETN_ACT_SILU: return z * sigmoid_f(z);
-        default: return z;
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    if constexpr (ACT == RETN_ACT_RELU) {
+        return z <= 0.f ? 0.f : z;
+    } else if constexpr (ACT == RETN_ACT_GELU) {
+        // z P(z) = max(z, 0) - |z| (1 - P(|z|))
+        float e;
+        const float a = fminf(fabsf(z), 16.f);
+        return fmaf(-a, normal_tail(a, e), z <= 0.f ? 0.f : z);
+    } else if constexpr (ACT == RETN_ACT_GELU_TANH) {
+        return z * sigmoid_f(tanh_arg(z));
+    } else {
+        return z * sigmoid_f(z);
     }
 }
-// The value and its derivative.
-__device__ __forceinline__ float act_slope(float z, int act, float& value) {
+// The derivative, and the value.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z, float& value) {
+    if constexpr (ACT == RETN_ACT_RELU) {
+        value = z <= 0.f ? 0.f : z;
+        return z > 0.f ? 1.f : 0.f;
+    } else if constexpr (ACT == RETN_ACT_GELU) {
+        const float c = cut(z, 16.f);
+        float e;
+        const float q = normal_tail(fabsf(c), e), p = c > 0.f ? 1.f - q : q;
+        value = z * p;
+        return fmaf(c * 0.3989422804014327f, e, p);
+    } else if constexpr (ACT == RETN_ACT_GELU_TANH) {
+        const float c = cut(z, 16.f), p = sigmoid_f(tanh_arg(c));
+        value = z * p;
+        return fmaf(c * p * (1.f - p), 1.5957691216057308f * fmaf(3.f * 0.044715f * c, c, 1.f), p);
+    } else {
+        const float c = cut(z, 100.f), p = sigmoid_f(c);
+        value = z * p;
+        return fmaf(c * p, 1.f - p, p);
+    }
+}
+template <int ACT>
+__device__ __forceinline__ void act_values_as(float (&z)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_value<ACT>(z[i]);
+}
+template <int ACT>
+__device__ __forceinline__ void act_slopes_as(float (&z)[8], float (&value)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_slope<ACT>(z[i], value[i]);
+}
+// z becomes its activation, in place.
+__device__ __forceinline__ void act_values(float (&z)[8], int act) {
     switch (act) {
-        case RETN_ACT_RELU: value = z <= 0.f ? 0.f : z; return z > 0.f ? 1.f : 0.f;
-        case RETN_ACT_GELU: {
-            const float c = cut(z, 16.f);
-            float e;
-            const float p = normal_cdf(c, e);
-            value = z * p;
-            return fmaf(c * 0.3989422804014327f, e, p);
-        }
-        case RETN_ACT_GELU_TANH: {
-            const float c = cut(z, 16.f), p = sigmoid_f(tanh_arg(c));
-            value = z * p;
-            return fmaf(c * p * (1.f - p), 1.5957691216057308f * fmaf(3.f * 0.044715f * c, c, 1.f), p);
-        }
-        case RETN_ACT_SILU: {
-            const float c = cut(z, 100.f), p = sigmoid_f(c);
-            value = z * p;
-            return fmaf(c * p, 1.f - p, p);
-        }
-        default: value = z; return 1.f;
+        case RETN_ACT_RELU: act_values_as<RETN_ACT_RELU>(z); break;
+        case RETN_ACT_GELU: act_values_as<RETN_ACT_GELU>(z); break;
+        case RETN_ACT_GELU_TANH: act_values_as<RETN_ACT_GELU_TANH>(z); break;
+        case RETN_ACT_SILU: act_values_as<RETN_ACT_SILU>(z); break;
+        default: break;
+    }
+}
+// z becomes the slope at z, in place, and `value` the activation of z.
+__device__ __forceinline__ void act_slopes(float (&z)[8], float (&value)[8], int act) {
+    switch (act) {
+        case RETN_ACT_RELU: act_slopes_as<RETN_ACT_RELU>(z, value); break;
+        case RETN_ACT_GELU: act_slopes_as<RETN_ACT_GELU>(z, value); break;
+        case RETN_ACT_GELU_TANH: act_slopes_as<RETN_ACT_GELU_TANH>(z, value); break;
+        case RETN_ACT_SILU: act_slopes_as<RETN_ACT_SILU>(z, value); break;
+        default:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                value[i] = z[i];
+                z[i] = 1.f;
+            }
     }
 }
 

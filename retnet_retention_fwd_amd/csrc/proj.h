@@ -23,7 +23,6 @@ struct ProjGroup {
     int M, N;                  // N also counts zero columns that a padded C takes,
     int bn;                    // this does not: B's columns
     int tiles_n, end;          // set by the launcher: column tiles, exclusive last tile
-    size_t part;               // set by the launcher: first element of its partial sums
 };
 
 // What happens to a product's sums.
@@ -48,9 +47,9 @@ struct ProjArgs {
     int ngroups;
     int red, red_rows, phases; // elements of the reduction; red counts zeros that pad rows to 16 bytes
     ProjEpi e;
-    int splits, per_split;     // set by the launcher: workgroups along the reduction, steps of each
-    int tiles, band;           // set by the launcher
-    float* part;               // partial sums of split reductions
+    int steps, tiles, band;    // set by the launcher: steps of a tile, tiles, rows of tiles walked together
+    int tiles1, splits1, splits2;   // set by the launcher: the first tiles1 are cut in splits1 parts, the others in splits2
+    float* part;               // parts of the sums of tiles that are cut
 };
 
 // Bytes of partial sums that a launch needs.

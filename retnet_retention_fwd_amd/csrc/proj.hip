@@ -35,19 +35,13 @@ namespace {
 
 constexpr uint32_t kOutside = 0x80000000u;   // a byte offset past every buffer resource here
 
-typedef float f32x4u_t __attribute__((ext_vector_type(4)));
-
 // c += a b over one fragment: 16 x 16 sums, 32 (bf16) or 16 (fp32) elements of the reduction.
 // Lane (g, l) = (lane / 16, lane % 16) brings row l of a and column l of b, 16 bytes of the
 // reduction from 16 g on, and holds columns ... of c as the matrix instructions do; which
 // elements meet in one instruction is the same for both operands, so any order will do.
-template <typename T, bool FIXED>
+template <typename T>
 __device__ __forceinline__ f32x4_t frag_mul(u16x8_t a, u16x8_t b, f32x4_t c) {
-    if constexpr (FIXED) {
-        static_assert(sizeof(T) == 2, "bf16");
-        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-        return c;
-    } else if constexpr (sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2) {
         return mfma16(a, b, c);
     } else {
         const f32x4_t x = __builtin_bit_cast(f32x4_t, a), y = __builtin_bit_cast(f32x4_t, b);
@@ -216,117 +210,225 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int left) {
     }
 }
 
-// Eight adjacent columns n .. n + 7 of row m (`v`, and `w`: the second projection's sums).
+// What a lane's eight columns n .. n + 7 have in every row.
 template <typename T, int KIND>
-__device__ __forceinline__ void finish8(const ProjEpi& e, const ProjGroup& g, int m, int n, float (&v)[8], float (&w)[8]) {
-    const int left = g.N - n;
-    const size_t at = static_cast<size_t>(m) * g.N + n;
-    T* c = static_cast<T*>(g.c) + static_cast<size_t>(m) * g.ldc + n;
-    if constexpr (KIND == kProjLinear) {
-        if (e.bias != nullptr) {
-            float b[8];
+struct Columns {
+    float bias[KIND == kProjLinear ? 8 : 1];
+    __device__ __forceinline__ void load(const ProjEpi& e, int n, int left) {
+        if constexpr (KIND == kProjLinear) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bias[i] = 0.f;
+            if (e.bias == nullptr || left <= 0) return;
             if (e.bias_f32)
-                load8<float>(static_cast<const float*>(e.bias) + n, left, b);
+                load8<float>(static_cast<const float*>(e.bias) + n, left, bias);
             else
-                load8<T>(static_cast<const T*>(e.bias) + n, left, b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += b[i];
+                load8<T>(static_cast<const T*>(e.bias) + n, left, bias);
         }
-        if (e.pre != nullptr) store8<T>(static_cast<T*>(e.pre) + at, v, left);
-        if (e.act != RETN_ACT_NONE) {
+    }
+};
+// R rows m[r] of eight adjacent columns n .. n + 7 (`v`, and `w`: the second projection's sums).
+// What a row reads is loaded for all rows first.
+template <typename T, int KIND, int R>
+__device__ __forceinline__ void finish(const ProjEpi& e, const ProjGroup& g, const Columns<T, KIND>& cols, const int (&m)[R], int n,
+                                       float (&v)[R][8], float (&w)[R][8]) {
+    const int left = g.N - n;
+    float x[R][8], u[R][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], e.act);
+    for (int r = 0; r < R; ++r) {
+        if (m[r] >= g.M) continue;
+        if constexpr (KIND == kProjLinear) {
+            if (e.res != nullptr) load8<T>(static_cast<const T*>(e.res) + static_cast<size_t>(m[r]) * g.N + n, left, x[r]);
+        } else if constexpr (KIND == kProjGatedBwd) {
+            const size_t ga = static_cast<size_t>(m[r]) * e.gate_ld + n;
+            load8<T>(static_cast<const T*>(e.gate) + ga, e.gate_n - n, x[r]);
+            load8<T>(static_cast<const T*>(e.up) + ga, e.gate_n - n, u[r]);
         }
-        if (e.res != nullptr) {
-            float r[8];
-            load8<T>(static_cast<const T*>(e.res) + at, left, r);
+    }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += r[i];
+    for (int r = 0; r < R; ++r) {
+        if (m[r] >= g.M) continue;
+        const size_t ca = static_cast<size_t>(m[r]) * g.ldc + n;
+        T* const c = static_cast<T*>(g.c) + ca;
+        if constexpr (KIND == kProjLinear) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[r][i] += cols.bias[i];
+            if (e.pre != nullptr) store8<T>(static_cast<T*>(e.pre) + static_cast<size_t>(m[r]) * g.N + n, v[r], left);
+            act_values(v[r], e.act);
+            if (e.res != nullptr) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[r][i] += x[r][i];
+            }
+            store8<T>(c, v[r], left);
+        } else if constexpr (KIND == kProjGated) {
+            // (columns of a padded product past gate's and up's are zero: both sums are)
+            const size_t ga = static_cast<size_t>(m[r]) * e.gate_ld + n;
+            if (e.gate != nullptr) store8<T>(static_cast<T*>(e.gate) + ga, v[r], e.gate_n - n);
+            if (e.up != nullptr) store8<T>(static_cast<T*>(e.up) + ga, w[r], e.gate_n - n);
+            act_values(v[r], e.act);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[r][i] *= w[r][i];
+            store8<T>(c, v[r], left);
+        } else {
+            float h[8], a[8];
+            act_slopes(x[r], a, e.act);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h[i] = a[i] * u[r][i];
+                x[r][i] *= v[r][i] * u[r][i];
+                v[r][i] *= a[i];
+            }
+            if (e.ggate != nullptr) store8<T>(static_cast<T*>(e.ggate) + ca, x[r], left);
+            if (e.gup != nullptr) store8<T>(static_cast<T*>(e.gup) + ca, v[r], left);
+            if (e.prod != nullptr) store8<T>(static_cast<T*>(e.prod) + ca, h, left);
         }
-        store8<T>(c, v, left);
-    } else if constexpr (KIND == kProjGated) {
-        // (columns of a padded product past gate's and up's are zero: both sums are)
-        const size_t ga = static_cast<size_t>(m) * e.gate_ld + n;
-        if (e.gate != nullptr) store8<T>(static_cast<T*>(e.gate) + ga, v, e.gate_n - n);
-        if (e.up != nullptr) store8<T>(static_cast<T*>(e.up) + ga, w, e.gate_n - n);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], e.act) * w[i];
-        store8<T>(c, v, left);
-    } else {
-        const size_t ga = static_cast<size_t>(m) * e.gate_ld + n, ca = static_cast<size_t>(m) * g.ldc + n;
-        float x[8], u[8], h[8], gx[8];
-        load8<T>(static_cast<const T*>(e.gate) + ga, e.gate_n - n, x);
-        load8<T>(static_cast<const T*>(e.up) + ga, e.gate_n - n, u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float a;
-            const float s = act_slope(x[i], e.act, a);
-            h[i] = a * u[i];
-            gx[i] = v[i] * u[i] * s;
-            v[i] = v[i] * a;
-        }
-        if (e.ggate != nullptr) store8<T>(static_cast<T*>(e.ggate) + ca, gx, left);
-        if (e.gup != nullptr) store8<T>(static_cast<T*>(e.gup) + ca, v, left);
-        if (e.prod != nullptr) store8<T>(static_cast<T*>(e.prod) + ca, h, left);
     }
 }
 
-__device__ __forceinline__ int round8(int n) { return (n + 7) & ~7; }
+// A wave's tile: TI x TJ blocks of 16 x 16 in each half of rows and of columns, and how its sums
+// become rows.  Lane (l16, g4) holds row l16 of a block and four columns; 16 rows at a time go
+// through LDS (turn: 16 rows of 64 floats, unit u of row r at u ^ r), so that a lane holds eight
+// adjacent columns of a row: the wave's columns of the left half, then of the right (pairs: the
+// two projections).
+template <typename T, int BM, int BN, int WM, int WN, int KIND>
+struct Rows {
+    static constexpr int TI = BM / 2 / WM / 16, TJ = BN / 2 / WN / 16, kWide = TJ * 16;
+    static constexpr bool PAIRS = KIND == kProjGated;
+    static constexpr int kTurn = 16 * 64 * 4;                        // bytes a wave
+    static constexpr int kUnits = (PAIRS ? 1 : 2) * kWide / 8, kRows = 64 / kUnits, kPass = 16 / kRows;
+    static constexpr int kCols = PAIRS ? BN / 2 : BN;                // columns of C of a tile
+    static_assert(TJ == 2, "64 columns a wave");
+
+    Columns<T, KIND> cols;
+    int n, lane, wm;
+    float* turn;
+
+    __device__ __forceinline__ void init(const ProjEpi& e, const ProjGroup& g, int n0, int wave, int lane_, char* smem) {
+        lane = lane_;
+        wm = wave / WN;
+        turn = reinterpret_cast<float*>(smem + wave * kTurn);
+        const int u = lane % kUnits;
+        n = n0 + u / (kWide / 8) * (BN / 2) + wave % WN * kWide + u % (kWide / 8) * 8;
+        cols.load(e, n, g.N - n);
+    }
+    // A row block's sums to the turning place.
+    __device__ __forceinline__ void write(const f32x4_t (&acc)[2][TJ]) const {
+        const int l16 = lane & 15, g4 = lane >> 4;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+                *reinterpret_cast<f32x4_t*>(turn + l16 * 64 + ((8 * y + 4 * j + g4) ^ l16) * 4) = acc[y][j];
+    }
+    // What follows for the written block i of half x.
+    __device__ __forceinline__ void put(const ProjEpi& e, const ProjGroup& g, int m0, int x, int i) const {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        float v[kPass][8], w[kPass][8];
+        int m[kPass];
+#pragma unroll
+        for (int q = 0; q < kPass; ++q) {
+            const int row = q * kRows + lane / kUnits, u = lane % kUnits * 2;
+            m[q] = m0 + x * (BM / 2) + (wm * TI + i) * 16 + row;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const f32x4_t a = *reinterpret_cast<const f32x4_t*>(turn + row * 64 + ((u + k) ^ row) * 4);
+                f32x4_t b{};
+                if (PAIRS) b = *reinterpret_cast<const f32x4_t*>(turn + row * 64 + ((u + k + 8) ^ row) * 4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    v[q][4 * k + r] = a[r];
+                    w[q][4 * k + r] = b[r];
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (n < g.N) finish<T, KIND, kPass>(e, g, cols, m, n, v, w);
+    }
+};
 
 // ---- the product ----------------------------------------------------------------------------------
-template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int WAVES, int KIND>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WAVES, WAVES))) void proj_kernel(const ProjArgs p) {
-    constexpr int NW = WM * WN, TI = BM / 2 / WM / 16, TJ = BN / 2 / WN / 16;   // blocks of a wave in a half
-    static_assert((TJ == 2 || TJ == 4) && TI <= 4, "a wave's tile is up to 128 x 128");
-    constexpr bool PAIRS = KIND == kProjGated;       // B's halves: the two projections
-    constexpr bool kFixed = WAVES == 1;
+// A launch's work: tiles, those of the last, partial round cut more finely along the reduction than
+// the others.  Workgroups (items) are numbered tile by tile within a part of the reduction, so that
+// those that run together walk the same columns of the operands.
+struct Item {
+    int tile, split, s0, s1;       // steps [s0, s1) of a tile
+    bool whole;
+};
+__device__ __forceinline__ Item item_of(const ProjArgs& p, int id) {
+    // XCD-aware order: launch ids rotate over the 8 XCDs; each XCD gets a contiguous range of a
+    // region's items, whose tiles are walked in bands of rows so that those in flight share both
+    // operands in its L2
+    const int first = p.tiles1 * p.splits1;
+    const bool late = id >= first;
+    const int base = late ? first : 0, tiles = late ? p.tiles - p.tiles1 : p.tiles1, splits = late ? p.splits2 : p.splits1;
+    const int total = tiles * splits;
+    int k = id - base;
+    const int x = k & 7, q = total >> 3, r = total & 7;
+    k = x * q + min(x, r) + (k >> 3);
+    Item it;
+    it.split = k / tiles;
+    it.tile = k % tiles + (late ? p.tiles1 : 0);
+    it.s0 = static_cast<int>(static_cast<long long>(p.steps) * it.split / splits);
+    it.s1 = static_cast<int>(static_cast<long long>(p.steps) * (it.split + 1) / splits);
+    it.whole = splits == 1;
+    return it;
+}
+// Where the part of a tile's sums is kept that split j leaves.
+__device__ __forceinline__ size_t part_of(const ProjArgs& p, int tile, int j) {
+    if (tile < p.tiles1) return static_cast<size_t>(j) * p.tiles1 + tile;
+    return static_cast<size_t>(p.splits1 > 1 ? p.splits1 : 0) * p.tiles1 + static_cast<size_t>(j) * (p.tiles - p.tiles1) + (tile - p.tiles1);
+}
+// A tile's place: its product, first row and column.
+struct Place {
+    int gi, m0, n0;
+};
+template <int BM, int COLS>
+__device__ __forceinline__ Place place_of(const ProjArgs& p, int t) {
+    Place at;
+    at.gi = 0;
+    if (p.ngroups > 1 && t >= p.g[0].end) at.gi = p.ngroups > 2 && t >= p.g[1].end ? 2 : 1;
+    const ProjGroup& g = p.g[at.gi];
+    if (at.gi > 0) t -= p.g[at.gi - 1].end;
+    const int tiles_m = (g.M + BM - 1) / BM, per = p.band * g.tiles_n, b = t / per, rem = t % per;
+    const int rows = min(p.band, tiles_m - b * p.band);
+    at.m0 = (b * p.band + rem % rows) * BM;
+    at.n0 = rem / rows * COLS;
+    return at;
+}
+
+template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int KIND>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void proj_kernel(const ProjArgs p) {
+    typedef Rows<T, BM, BN, WM, WN, KIND> Out;
+    constexpr int NW = WM * WN, TI = Out::TI, TJ = Out::TJ;       // blocks of a wave in a half
+    static_assert(TI == 2 || TI == 4, "a wave's tile is up to 128 x 64");
+    constexpr bool PAIRS = Out::PAIRS;               // B's halves: the two projections
     typedef Half<T, AR, BM / 2, NW> A;
     typedef Half<T, BR, BN / 2, NW> B;
     // LDS of a stage: A's upper and lower, B's left and right half
     constexpr int kStage = 2 * (A::kBytes + B::kBytes), kAb = A::kBytes, kBl = 2 * A::kBytes, kBr = kBl + B::kBytes;
     constexpr int kEs = sizeof(T), kStep = 128 / kEs;
+    constexpr int kCA = A::kCopies, kCB = B::kCopies, kPair = kCA + kCB;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l16 = lane & 15, g4 = lane >> 4, wm = wave / WN, wn = wave % WN;
+    const int wm = wave / WN, wn = wave % WN;
 
-    // XCD-aware order: launch ids rotate over the 8 XCDs; each XCD gets a contiguous range of
-    // tiles, walked in bands of rows so that the tiles in flight share both operands in its L2
-    const int total = p.tiles * p.splits;
-    int id = blockIdx.x;
-    {
-        const int x = id & 7, q = total >> 3, r = total & 7;
-        id = x * q + min(x, r) + (id >> 3);
-    }
-    const int split = id / p.tiles;
-    int t = id % p.tiles, gi = 0;
-    if (p.ngroups > 1 && t >= p.g[0].end) gi = p.ngroups > 2 && t >= p.g[1].end ? 2 : 1;
-    const ProjGroup& g = p.g[gi];
-    if (gi > 0) t -= p.g[gi - 1].end;
-    const int tiles_n = g.tiles_n;
-    constexpr int kCols = PAIRS ? BN / 2 : BN;       // columns of C of a tile
-    const int tiles_m = (g.M + BM - 1) / BM;
-    const int per = p.band * tiles_n, b0 = t / per, rem = t % per, brows = min(p.band, tiles_m - b0 * p.band);
-    const int m0 = (b0 * p.band + rem % brows) * BM, n0 = (rem / brows) * kCols;
+    const Item it = item_of(p, blockIdx.x);
+    const Place at = place_of<BM, Out::kCols>(p, it.tile);
+    const ProjGroup& g = p.g[at.gi];
+    const int s0 = it.s0, s1 = it.s1;
+    const int red = held(p.red), red_rows = held(p.red_rows), nk1 = (red + kStep - 1) / kStep;
+    const uint32_t lds0 = lds_addr_of(smem);
 
     A sa;
     B sb;
-    sa.init(wave, lane, wm * TI, g.lda);
-    sb.init(wave, lane, wn * TJ, g.ldb);
-
-    const int nk1 = (p.red + kStep - 1) / kStep;
-    const int s0 = split * p.per_split, s1 = min(s0 + p.per_split, nk1 * p.phases);
     Operand<T, AR, BM / 2> oa;
     Operand<T, BR, BN / 2> ob;       // pairs: the halves are the two projections, at the same columns
-    oa.init(g.a, p.phases > 1 ? g.a2 : g.a, g.lda, m0, g.M, p.red);
-    ob.init(g.b, PAIRS || p.phases > 1 ? g.b2 : g.b, g.ldb, n0, g.bn, p.red);
-    if (PAIRS) {
-        ob.half = held(ob.second - ob.first);
-        ob.size[1] = ob.size[0];
-    }
-    const int red = held(p.red), red_rows = held(p.red_rows);
     // Sources of step kt.  Steps follow each other by `next` except at the ends of a phase and of
-    // this workgroup's part: `turn` is the next such step.
+    // the tile's steps: `turn_at` is the next such step.
     int turn_at = 0;
     auto source = [&](int kt) {
         if (kt != turn_at) {
@@ -340,14 +442,21 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
         ob.go(k, two && !PAIRS, red, red_rows, kt < s1);
         turn_at = kt >= s1 ? kt + 1 : min(s1, k >= nk1 - 1 ? kt + 1 : kt + (nk1 - 1 - k));
     };
-    const uint32_t lds0 = lds_addr_of(smem);
-    auto copy = [&](const auto& side, const auto& from, bool red, int h, int i, uint32_t at) {
-        const uint32_t o = red && side.unit >= from.units ? kOutside : side.off[i];
+    auto copy = [&](const auto& side, const auto& from, bool by_red, int h, int i, uint32_t at) {
+        const uint32_t o = by_red && side.unit >= from.units ? kOutside : side.off[i];
         buf2lds16(from.rs[h], o, from.soff, at + (wave + NW * i) * 1024);
     };
     // copy i of half h of A, of B, into the stage at `st`
     auto copy_a = [&](int h, int i, uint32_t st) { copy(sa, oa, AR, h, i, st + h * kAb); };
     auto copy_b = [&](int h, int i, uint32_t st) { copy(sb, ob, BR, h, i, st + (h ? kBr : kBl)); };
+    sa.init(wave, lane, wm * TI, g.lda);
+    sb.init(wave, lane, wn * TJ, g.ldb);
+    oa.init(g.a, p.phases > 1 ? g.a2 : g.a, g.lda, at.m0, g.M, red);
+    ob.init(g.b, PAIRS || p.phases > 1 ? g.b2 : g.b, g.ldb, at.n0, g.bn, red);
+    if (PAIRS) {
+        ob.half = held(ob.second - ob.first);
+        ob.size[1] = ob.size[0];
+    }
 
     f32x4_t acc[2][TI][2][TJ];
 #pragma unroll
@@ -358,9 +467,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
             for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int j = 0; j < TJ; ++j) acc[x][i][y][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    if (s0 < s1) {
-        constexpr int kCA = A::kCopies, kCB = B::kCopies, kPair = kCA + kCB;
+    {
         turn_at = s0;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -398,7 +505,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
 #pragma unroll
             for (int n = 0; n < kMul; ++n) {
                 const int j = n % TJ, e = n / TJ % 2, ks = n / (2 * TJ) % 2, i = n / (4 * TJ) * 2 + e;
-                acc[X][i][Y][j] = frag_mul<T, kFixed>(fb[BX][j][ks], fa[X][i][ks], acc[X][i][Y][j]);
+                acc[X][i][Y][j] = frag_mul<T>(fb[BX][j][ks], fa[X][i][ks], acc[X][i][Y][j]);
                 if (n < kReads) {
                     if constexpr (RA)
                         fa[H][n >> 1][n & 1] = sa.read(in, n >> 1, n & 1);
@@ -444,196 +551,195 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WA
             step(kt + 1, c1);
         }
         if (kt < s1) step(kt, c0);
-        if constexpr (kFixed) {
-            asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int i = 0; i < TI; ++i)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int j = 0; j < TJ; ++j) asm volatile("" : "+a"(acc[x][i][y][j]));
-        }
-        wait_vmcnt<0>();               // (the empty copies past the end, before LDS has other uses)
-    }
-    __syncthreads();   // the stages become the waves' turning places
+        wait_vmcnt<0>();               // (the empty copies past the end,
+        lds_barrier();                 // for all waves, before their places are filled again)
 
-    // The sums of 16 rows at a time go through LDS, so that a lane holds eight adjacent columns
-    // of a row: the wave's columns of the left half, then of the right.
-    constexpr int kWide = TJ * 16, kPitch = 2 * kWide + 4;
-    constexpr int kUnits = (PAIRS ? 1 : 2) * kWide / 8, kRows = 64 / kUnits;
-    float* const turn = reinterpret_cast<float*>(smem) + wave * 16 * kPitch;
-    const int np = round8(g.N);
-    auto put = [&](auto half) {
-        constexpr int x = half();
-#pragma unroll
-        for (int i = 0; i < TI; ++i) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int j = 0; j < TJ; ++j)
-                    *reinterpret_cast<f32x4_t*>(turn + l16 * kPitch + kWide * y + 16 * j + 4 * g4) = acc[x][i][y][j];
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+    if (it.whole) {
+        Out out;
+        out.init(p.e, g, at.n0, wave, lane, smem);
+        // (a loop, as what follows the sums is long: eight copies of it are more than the
+        // instruction cache holds, 25 us of 120 at 8192 x 4096 x 1024 with gelu)
 #pragma unroll 1
-            for (int q = 0; q < 16 / kRows; ++q) {
-                const int row = q * kRows + lane / kUnits, u = lane % kUnits;
-                const float* src = turn + row * kPitch + u * 8;
-                float v[8], w[8];
+        for (int b = 0; b < 2 * TI; ++b) {
+            const int now = held(b);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const f32x4_t e = *reinterpret_cast<const f32x4_t*>(src + 4 * k);
-                    f32x4_t f{};
-                    if (PAIRS) f = *reinterpret_cast<const f32x4_t*>(src + kWide + 4 * k);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        v[4 * k + r] = e[r];
-                        w[4 * k + r] = f[r];
-                    }
-                }
-                const int m = m0 + x * (BM / 2) + (wm * TI + i) * 16 + row;
-                const int n = n0 + u / (kWide / 8) * (BN / 2) + wn * kWide + u % (kWide / 8) * 8;
-                if (m >= g.M || n >= g.N) continue;
-                if (p.splits > 1) {
-                    const size_t plane = static_cast<size_t>(g.M) * np;
-                    float* o = p.part + g.part + split * plane * (PAIRS ? 2 : 1) + static_cast<size_t>(m) * np + n;
-                    store8<float>(o, v, 8);
-                    if (PAIRS) store8<float>(o + plane, w, 8);
-                } else {
-                    finish8<T, KIND>(p.e, g, m, n, v, w);
-                }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            for (int k = 0; k < 2 * TI; ++k)
+                if (now == k) out.write(acc[k / TI][k % TI]);
+            out.put(p.e, g, at.m0, now / TI, now % TI);
         }
-    };
-    put(std::integral_constant<int, 0>());
-    put(std::integral_constant<int, 1>());
+    } else {
+        // a part of a tile's sums, as the lanes hold them
+        f32x4_t* o = reinterpret_cast<f32x4_t*>(p.part) + (part_of(p, it.tile, it.split) * NW + wave) * (4 * TI * TJ) * 64 + lane;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int j = 0; j < TJ; ++j) o[(((x * TI + i) * 2 + y) * TJ + j) * 64] = acc[x][i][y][j];
+    }
 }
 
-// Sums of split reductions, in the order of the splits.
-template <typename T, int KIND>
-__global__ __launch_bounds__(256) void proj_join_kernel(const ProjArgs p) {
-    const ProjGroup& g = p.g[blockIdx.y];
-    const int np = round8(g.N), units = np / 8;
-    const size_t plane = static_cast<size_t>(g.M) * np, total = static_cast<size_t>(g.M) * units;
-    for (size_t e = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; e < total; e += static_cast<size_t>(gridDim.x) * 256) {
-        const int m = static_cast<int>(e / units), n = static_cast<int>(e % units) * 8;
-        const float* src = p.part + g.part + static_cast<size_t>(m) * np + n;
-        float v[8] = {}, w[8] = {};
+// The sums of tiles whose reduction is cut, added in the order of the cuts.  A workgroup per tile
+// and 16-row block of its waves.
+template <typename T, int BM, int BN, int WM, int WN, int KIND>
+__global__ __launch_bounds__(64 * WM * WN) void proj_join_kernel(const ProjArgs p) {
+    typedef Rows<T, BM, BN, WM, WN, KIND> Out;
+    constexpr int NW = WM * WN, TI = Out::TI, TJ = Out::TJ;
+    __shared__ __attribute__((aligned(1024))) char smem[NW * Out::kTurn];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = blockIdx.x + (p.splits1 > 1 ? 0 : p.tiles1), xi = blockIdx.y;
+    const int splits = t < p.tiles1 ? p.splits1 : p.splits2;
+    if (splits == 1) return;
+    const Place at = place_of<BM, Out::kCols>(p, t);
+    const ProjGroup& g = p.g[at.gi];
+    f32x4_t acc[2][TJ];
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[y][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-        for (int s = 0; s < p.splits; ++s) {
-            float x[8];
-            load8<float>(src, 8, x);
+    for (int j = 0; j < splits; ++j) {
+        const f32x4_t* o = reinterpret_cast<const f32x4_t*>(p.part) + (part_of(p, t, j) * NW + wave) * (4 * TI * TJ) * 64 + lane;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += x[i];
-            src += plane;
-            if (KIND == kProjGated) {
-                load8<float>(src, 8, x);
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] += x[i];
-                src += plane;
-            }
-        }
-        finish8<T, KIND>(p.e, g, m, n, v, w);
+            for (int k = 0; k < TJ; ++k) acc[y][k] += o[((xi * 2 + y) * TJ + k) * 64];
     }
+    Out out;
+    out.init(p.e, g, at.n0, wave, lane, smem);
+    out.write(acc);
+    out.put(p.e, g, at.m0, xi / TI, xi % TI);
+}
+
+// Products over nothing (no rows in a gradient of weights): zeros.
+template <typename T>
+__global__ __launch_bounds__(256) void proj_zero_kernel(const ProjArgs p) {
+    const ProjGroup& g = p.g[blockIdx.y];
+    const size_t total = static_cast<size_t>(g.M) * g.N;
+    for (size_t e = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; e < total; e += static_cast<size_t>(gridDim.x) * 256)
+        static_cast<T*>(g.c)[e / g.N * g.ldc + e % g.N] = T(0);
 }
 
 // ---- plan ---------------------------------------------------------------------------------------
+// Tiles: 256 x 256 reach 1.35 PFLOP/s in the main loop, 256 x 128 1.25, 128 x 128 (two workgroups
+// a CU) 1.15; fp32 a tenth of that for any.
 struct Tile {
     int bm, bn, slots;     // workgroups of the chip at a time
-    double rate;           // of the chip's matrix rate that the main loop reaches
+    double rate;           // PFLOP/s of the main loop
+    double tail;           // microseconds of a workgroup that do not overlap with others: first copies, last stores
 };
-constexpr Tile kTiles[2] = {{256, 256, 256, 1.0}, {128, 128, 512, 0.75}};
+constexpr Tile kTiles[3] = {{256, 256, 256, 1.35, 9.0}, {256, 128, 256, 1.25, 6.0}, {128, 128, 512, 1.15, 5.0}};
+constexpr double kRateF32 = 0.135;
 
-// Sets tiles, splits and bands; returns the tile's number.  Estimated time: rounds of
-// workgroups, each its steps and a fixed part, then the join's traffic.
+// Sets tiles and how they are cut; returns the tile's number.  All tiles are cut into splits1 parts
+// of the reduction; the whole rounds of workgroups that this makes are taken as they are, the rest
+// of the tiles are cut into splits2 parts, as many as fill the chip once.
 int plan(ProjArgs& a, ProjKind kind, bool bf16) {
     const int step = bf16 ? 64 : 32;
-    const int steps = (a.red + step - 1) / step * a.phases;
-    int best = 0, best_splits = 1;
+    a.steps = (a.red + step - 1) / step * a.phases;
+    int best = 0;
     double best_t = 1e30;
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < 3; ++c) {
         const Tile& t = kTiles[c];
         const int cols = kind == kProjGated ? t.bn / 2 : t.bn;
-        double tiles = 0, out = 0;
-        for (int i = 0; i < a.ngroups; ++i) {
-            tiles += static_cast<double>((a.g[i].M + t.bm - 1) / t.bm) * ((a.g[i].N + cols - 1) / cols);
-            out += static_cast<double>(a.g[i].M) * a.g[i].N * (kind == kProjGated ? 2 : 1);
-        }
-        // microseconds of a step in a full chip: its matrix instructions at 1.4 (0.13) PFLOP/s
-        const double us = 2.0 * t.bm * t.bn * step * t.slots / (t.rate * (bf16 ? 1.4e9 : 0.13e9));
-        for (int s = 1; s <= 16 && s <= steps; ++s) {
-            if (s > 1 && tiles * s > 2 * t.slots) break;
-            const int per = (steps + s - 1) / s;
-            if ((steps + per - 1) / per != s) continue;
-            const double rounds = ceil(tiles * s / t.slots);
-            double time = rounds * (per * us + 2.0) + 2.0;
-            if (s > 1) time += 3.0 + out * s * 8 / 3e6;
-            if (time < best_t) {
-                best_t = time;
-                best = c;
-                best_splits = s;
+        long long tiles = 0;
+        for (int i = 0; i < a.ngroups; ++i)
+            tiles += static_cast<long long>((a.g[i].M + t.bm - 1) / t.bm) * ((a.g[i].N + cols - 1) / cols);
+        // microseconds of so many steps with so many workgroups (two share a CU where there are more than CUs)
+        auto time = [&](long long groups, int steps) {
+            const double full = 2.0 * t.bm * t.bn * step * 256 / ((bf16 ? t.rate : kRateF32) * 1e9);
+            return steps * full * std::max(1.0, std::min<double>(groups, t.slots) / 256) + t.tail;
+        };
+        for (int s1 = 1; s1 <= 32 && s1 <= std::max(a.steps, 1); ++s1) {
+            const long long items = tiles * s1;
+            if (s1 > 1 && items > 4 * t.slots) break;
+            const int per1 = (a.steps + s1 - 1) / s1;
+            for (int cut = 0; cut < 2; ++cut) {
+                // the last round: as it comes, or cut
+                long long t1 = tiles, t2 = 0;
+                int s2 = 1;
+                double us = static_cast<double>((items + t.slots - 1) / t.slots) * time(items, per1);
+                if (cut) {
+                    t1 = items / t.slots * t.slots / s1;
+                    t2 = tiles - t1;
+                    if (t2 == 0) continue;
+                    s2 = static_cast<int>(std::min<long long>(std::min(a.steps, 32), t.slots / t2));
+                    if (s2 <= s1) continue;
+                    us = static_cast<double>(items / t.slots) * time(items, per1) + time(t2 * s2, (a.steps + s2 - 1) / s2);
+                }
+                const double parts = (s1 > 1 ? static_cast<double>(t1) * s1 : 0) + (s2 > 1 ? static_cast<double>(t2) * s2 : 0);
+                if (parts > 0) us += 5.0 + parts * t.bm * t.bn * 8 / 3.5e6;
+                if (us < best_t) {
+                    best_t = us;
+                    best = c;
+                    a.tiles1 = static_cast<int>(t1);
+                    a.splits1 = s1;
+                    a.splits2 = s2;
+                }
             }
         }
     }
     const Tile& t = kTiles[best];
-    a.splits = best_splits;
-    a.per_split = (steps + best_splits - 1) / best_splits;
     a.band = 8;
     int tiles = 0;
-    size_t part = 0;
     for (int i = 0; i < a.ngroups; ++i) {
         ProjGroup& g = a.g[i];
         const int cols = kind == kProjGated ? t.bn / 2 : t.bn;
         g.tiles_n = (g.N + cols - 1) / cols;
         tiles += (g.M + t.bm - 1) / t.bm * g.tiles_n;
         g.end = tiles;
-        g.part = part;
-        part += static_cast<size_t>(a.splits) * g.M * ((g.N + 7) & ~7) * (kind == kProjGated ? 2 : 1);
     }
     a.tiles = tiles;
     return best;
 }
+// Parts of sums that cut tiles leave.
+size_t parts_of(const ProjArgs& a) {
+    const size_t t1 = a.tiles1, t2 = a.tiles - a.tiles1;
+    return (a.splits1 > 1 ? t1 * a.splits1 : 0) + (a.splits2 > 1 ? t2 * a.splits2 : 0);
+}
 
-template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int WAVES, int KIND>
+template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int KIND>
 hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
     constexpr int lds = 2 * (BM + BN) * 128;
+    static_assert(lds >= WM * WN * Rows<T, BM, BN, WM, WN, KIND>::kTurn, "turning places");
+    const int items = a.tiles1 * a.splits1 + (a.tiles - a.tiles1) * a.splits2;
     static std::once_flag attr_once;   // thread-safe one-time init of the LDS limit
     std::call_once(attr_once, [] {
-        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&proj_kernel<T, AR, BR, BM, BN, WM, WN, WAVES, KIND>),
+        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&proj_kernel<T, AR, BR, BM, BN, WM, WN, KIND>),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     });
     {
         ProfScope prof(kProfProj, st);
-        hipLaunchKernelGGL((proj_kernel<T, AR, BR, BM, BN, WM, WN, WAVES, KIND>), dim3(a.tiles * a.splits), dim3(64 * WM * WN), lds,
-                           st, a);
+        hipLaunchKernelGGL((proj_kernel<T, AR, BR, BM, BN, WM, WN, KIND>), dim3(items), dim3(64 * WM * WN), lds, st, a);
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
-    size_t most = 0;
-    for (int i = 0; i < a.ngroups; ++i) most = std::max(most, static_cast<size_t>(a.g[i].M) * ((a.g[i].N + 7) / 8));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || parts_of(a) == 0) return e;
     ProfScope prof(kProfReduce, st);
-    const unsigned blocks = static_cast<unsigned>(std::min<size_t>((most + 255) / 256, 1u << 16));
-    hipLaunchKernelGGL((proj_join_kernel<T, KIND>), dim3(blocks, a.ngroups), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((proj_join_kernel<T, BM, BN, WM, WN, KIND>), dim3(a.splits1 > 1 ? a.tiles : a.tiles - a.tiles1, BM / WM / 16),
+                       dim3(64 * WM * WN), 0, st, a);
     return hipGetLastError();
 }
 
 template <typename T, bool AR, bool BR, int KIND>
 hipError_t launch_sized(const ProjArgs& a, int tile, hipStream_t st) {
-    if constexpr (sizeof(T) == 2) {
-        if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st);
-    } else {
-        if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st);
-    }
-    return launch_tile<T, AR, BR, 128, 128, 2, 2, 2, KIND>(a, st);
+    if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, KIND>(a, st);
+    if (tile == 1) return launch_tile<T, AR, BR, 256, 128, 4, 2, KIND>(a, st);
+    return launch_tile<T, AR, BR, 128, 128, 2, 2, KIND>(a, st);
 }
 
 template <typename T>
 hipError_t launch_typed(const ProjArgs& a, int tile, ProjKind kind, bool a_red, bool b_red, hipStream_t st) {
+    if (a.steps == 0) {
+        size_t most = 0;
+        for (int i = 0; i < a.ngroups; ++i) most = std::max(most, static_cast<size_t>(a.g[i].M) * a.g[i].N);
+        ProfScope prof(kProfProjPass, st);
+        const unsigned blocks = static_cast<unsigned>(std::min<size_t>((most + 255) / 256, 1u << 14));
+        hipLaunchKernelGGL((proj_zero_kernel<T>), dim3(blocks, a.ngroups), dim3(256), 0, st, a);
+        return hipGetLastError();
+    }
     if (kind == kProjGated) return launch_sized<T, true, true, kProjGated>(a, tile, st);
     if (kind == kProjGatedBwd) return launch_sized<T, true, false, kProjGatedBwd>(a, tile, st);
     if (a_red) return b_red ? launch_sized<T, true, true, kProjLinear>(a, tile, st) : launch_sized<T, true, false, kProjLinear>(a, tile, st);
@@ -693,12 +799,10 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, int lpr, size_t
             if (a.pre != nullptr) {
                 float z[8] = {};
                 if (left > 0) load8<T>(static_cast<const T*>(a.pre) + r * a.N + n, left, z);
+                float v[8];
+                act_slopes(z, v, a.act);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float v;
-                    const float d = act_slope(z[i], a.act, v);
-                    g[i] = i < left ? g[i] * d : 0.f;
-                }
+                for (int i = 0; i < 8; ++i) g[i] = i < left ? g[i] * z[i] : 0.f;
             }
             if (pad) store8<T>(static_cast<T*>(a.gz) + r * a.ldz + n, g, static_cast<int>(a.ldz) - n);
 #pragma unroll
@@ -722,12 +826,8 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, int lpr, size_t
 
 size_t proj_partial_bytes(const ProjArgs& args, ProjKind kind, bool bf16) {
     ProjArgs a = args;
-    (void)plan(a, kind, bf16);
-    if (a.splits == 1) return 0;
-    size_t n = 0;
-    for (int i = 0; i < a.ngroups; ++i)
-        n += static_cast<size_t>(a.splits) * a.g[i].M * ((a.g[i].N + 7) & ~7) * (kind == kProjGated ? 2 : 1);
-    return n * sizeof(float);
+    const Tile& t = kTiles[plan(a, kind, bf16)];
+    return a.steps == 0 ? 0 : parts_of(a) * t.bm * t.bn * sizeof(float);
 }
 
 hipError_t launch_proj(ProjArgs a, ProjKind kind, bool bf16, bool a_red, bool b_red, hipStream_t st) {
