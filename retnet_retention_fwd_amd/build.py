@@ -20,7 +20,7 @@ LIB_NAME = "libretention_fwd.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["api.cpp", "profile.cpp", "backward.cpp", "generic_chunk.hip", "decode.hip", "mfma_chunk.hip", "chunk64.hip", "chunkw.hip", "calib.hip", "noalloc.hip",
-           "bwd_kernels.hip", "msr.hip", "block_api.cpp", "norm.hip", "rotary.hip", "conv.hip", "scan.hip", "scan_bwd.hip", "proj_api.cpp", "proj.hip",
+           "bwd_kernels.hip", "msr.hip", "block_api.cpp", "norm.hip", "rotary.hip", "conv.hip", "scan.hip", "scan_bwd.hip", "proj_api.cpp", "proj.hip", "proj_small.hip",
            "heads.hip"]
 
 # Packed-fp32 instructions are disabled for all device code (the compiler would

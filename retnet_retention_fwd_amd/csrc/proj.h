@@ -58,8 +58,10 @@ size_t proj_partial_bytes(const ProjArgs& a, ProjKind kind, bool bf16);
 // reduction-major A.
 hipError_t launch_proj(ProjArgs a, ProjKind kind, bool bf16, bool a_red, bool b_red, hipStream_t st);
 
-// Few rows (tokens of a decoding batch).
-bool proj_small(int M, int N, int K, bool bf16);
+// Products of few rows, x W^T (linear and gated): operands of any alignment, red_rows elements of
+// the reduction, no partial sums.
+bool proj_small(int M);
+hipError_t launch_proj_small(const ProjArgs& a, ProjKind kind, bool bf16, hipStream_t st);
 
 // dst[rows][ldd] = src[rows][lds] of `width` elements, zeros behind them.
 hipError_t launch_proj_pack(const void* src, long long lds, void* dst, long long ldd, size_t rows, int width, bool bf16,

@@ -68,6 +68,10 @@ struct Call {
         if (err == hipSuccess) err = retn::launch_proj_pack(p, ld, ws + at, w, n, width, bf16, st);
         return Rows{ws + at, w};
     }
+    // x W^T of few rows, read as they lie
+    void small(const ProjArgs& a, retn::ProjKind kind) {
+        if (err == hipSuccess) err = retn::launch_proj_small(a, kind, bf16, st);
+    }
     void product(const ProjArgs& a, retn::ProjKind kind, bool a_red, bool b_red) {
         if (err == hipSuccess) err = retn::launch_proj(a, kind, bf16, a_red, b_red, st);
     }
@@ -109,6 +113,7 @@ struct LinearPlan {
 LinearPlan linear_plan(int M, int N, int K, bool bf16, bool aligned) {
     const size_t es = bf16 ? 2 : 4;
     LinearPlan p{};
+    if (retn::proj_small(M)) return p;
     Layout l;
     p.x = l.take(aligned ? 0 : sz(M) * padded(K, bf16) * es);
     p.w = l.take(aligned ? 0 : sz(N) * padded(K, bf16) * es);
@@ -140,6 +145,11 @@ FfnPlan ffn_plan(int M, int D, int F, bool bf16, bool aligned) {
     const size_t es = bf16 ? 2 : 4;
     FfnPlan p{};
     Layout l;
+    if (retn::proj_small(M)) {
+        p.h = l.take(sz(M) * padded(F, bf16) * es);
+        p.total = l.total;
+        return p;
+    }
     p.x = l.take(aligned ? 0 : sz(M) * padded(D, bf16) * es);
     p.wg = l.take(aligned ? 0 : sz(F) * padded(D, bf16) * es);
     p.wu = l.take(aligned ? 0 : sz(F) * padded(D, bf16) * es);
@@ -303,8 +313,10 @@ retn_status linear_fwd(const void* x, long long ldx, const void* weight, const v
     if (clash(in, outs)) return RETN_ERR_ALIAS;
     if (bad_workspace(workspace, workspace_bytes, p.total)) return RETN_ERR_WORKSPACE;
     Call c{bf16, es, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)};
-    const Rows rx = c.rows(x, ldx, sz(M), K, p.x), rw = c.rows(weight, K, sz(N), K, p.w);
-    const int red = padded(K, bf16);
+    const bool small = retn::proj_small(M);
+    const Rows rx = small ? Rows{x, ldx} : c.rows(x, ldx, sz(M), K, p.x);
+    const Rows rw = small ? Rows{weight, K} : c.rows(weight, K, sz(N), K, p.w);
+    const int red = small ? K : padded(K, bf16);
     ProjArgs a = product_of(red, red);
     a.g[0] = group(rx, rw, y, N, M, N, N);
     a.e.bias = bias;
@@ -313,7 +325,10 @@ retn_status linear_fwd(const void* x, long long ldx, const void* weight, const v
     a.e.res = residual;
     a.e.pre = pre;
     a.part = reinterpret_cast<float*>(c.ws + p.part);
-    c.product(a, retn::kProjLinear, true, true);
+    if (small)
+        c.small(a, retn::kProjLinear);
+    else
+        c.product(a, retn::kProjLinear, true, true);
     return done(c.err);
 }
 
@@ -413,9 +428,11 @@ retn_status gated_ffn_fwd(const void* x, long long ldx, const void* w_gate, cons
     if (clash(in, outs)) return RETN_ERR_ALIAS;
     if (bad_workspace(workspace, workspace_bytes, p.total)) return RETN_ERR_WORKSPACE;
     Call c{bf16, es, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)};
-    const Rows rx = c.rows(x, ldx, sz(M), D, p.x), rg = c.rows(w_gate, D, sz(F), D, p.wg),
-               ru = c.rows(w_up, D, sz(F), D, p.wu);
-    const int rd = padded(D, bf16), rf = padded(F, bf16);
+    const bool small = retn::proj_small(M);
+    const Rows rx = small ? Rows{x, ldx} : c.rows(x, ldx, sz(M), D, p.x);
+    const Rows rg = small ? Rows{w_gate, D} : c.rows(w_gate, D, sz(F), D, p.wg);
+    const Rows ru = small ? Rows{w_up, D} : c.rows(w_up, D, sz(F), D, p.wu);
+    const int rd = small ? D : padded(D, bf16), rf = padded(F, bf16);
     const Rows h{c.ws + p.h, rf};
     float* const part = reinterpret_cast<float*>(c.ws + p.part);
     ProjArgs a = product_of(rd, rd);
@@ -427,12 +444,19 @@ retn_status gated_ffn_fwd(const void* x, long long ldx, const void* w_gate, cons
     a.e.gate_ld = F;
     a.e.gate_n = F;
     a.part = part;
-    c.product(a, retn::kProjGated, true, true);
-    ProjArgs b = product_of(rf, rf);
-    b.g[0] = group(h, c.rows(w_down, F, sz(D), F, p.wd), y, D, M, D, D);
+    if (small)
+        c.small(a, retn::kProjGated);
+    else
+        c.product(a, retn::kProjGated, true, true);
+    const int rr = small ? F : rf;
+    ProjArgs b = product_of(rr, rr);
+    b.g[0] = group(h, small ? Rows{w_down, F} : c.rows(w_down, F, sz(D), F, p.wd), y, D, M, D, D);
     b.e.res = residual;
     b.part = part;
-    c.product(b, retn::kProjLinear, true, true);
+    if (small)
+        c.small(b, retn::kProjLinear);
+    else
+        c.product(b, retn::kProjLinear, true, true);
     return done(c.err);
 }
 
