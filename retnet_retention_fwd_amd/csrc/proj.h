@@ -60,7 +60,7 @@ hipError_t launch_proj(ProjArgs a, ProjKind kind, bool bf16, bool a_red, bool b_
 
 // Products of few rows, x W^T (linear and gated): operands of any alignment, red_rows elements of
 // the reduction, no partial sums.
-bool proj_small(int M);
+bool proj_small(int M, int N);
 hipError_t launch_proj_small(const ProjArgs& a, ProjKind kind, bool bf16, hipStream_t st);
 
 // dst[rows][ldd] = src[rows][lds] of `width` elements, zeros behind them.

@@ -255,8 +255,8 @@ __device__ __forceinline__ Item item_of(const ProjArgs& p, int id) {
     Item it;
     it.split = k / tiles;
     it.tile = k % tiles + (late ? p.tiles1 : 0);
-    it.s0 = static_cast<int>(static_cast<long long>(p.steps) * it.split / splits);
-    it.s1 = static_cast<int>(static_cast<long long>(p.steps) * (it.split + 1) / splits);
+    it.s0 = p.steps * it.split / splits;         // (2^24 steps, 32 splits at most)
+    it.s1 = p.steps * (it.split + 1) / splits;
     it.whole = splits == 1;
     return it;
 }
@@ -283,7 +283,7 @@ __device__ __forceinline__ Place place_of(const ProjArgs& p, int t) {
     return at;
 }
 
-template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int KIND>
+template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int STAGES, int KIND>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void proj_kernel(const ProjArgs p) {
     typedef Rows<T, BM, BN, WM, WN, KIND> Out;
     constexpr int NW = WM * WN, TI = Out::TI, TJ = Out::TJ;       // blocks of a wave in a half
@@ -295,6 +295,8 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     constexpr int kStage = 2 * (A::kBytes + B::kBytes), kAb = A::kBytes, kBl = 2 * A::kBytes, kBr = kBl + B::kBytes;
     constexpr int kEs = sizeof(T), kStep = 128 / kEs;
     constexpr int kCA = A::kCopies, kCB = B::kCopies, kPair = kCA + kCB;
+    constexpr int kWait = (2 * STAGES - 2) * kPair;  // copies younger than those that a barrier waits for
+    static_assert(kWait < 64, "the counter's range");
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -354,7 +356,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     {
         turn_at = s0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < STAGES; ++k) {
             source(s0 + k);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -364,8 +366,8 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
                 for (int i = 0; i < kCB; ++i) copy_b(h, i, lds0 + k * kStage);
             }
         }
-        source(s0 + 2);
-        wait_vmcnt<2 * kPair>();
+        source(s0 + STAGES);
+        wait_vmcnt<kWait>();
         lds_barrier();
         u16x8_t fa[2][TI][2], fb[2][TJ][2];          // A: upper, lower; B: by turns left and right
 #pragma unroll
@@ -414,7 +416,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
             quarter(c0, c1, r, c1, c1, cur + kAb, [&](int i) {
                 if (i < kCB) copy_b(0, i, cur);
             });
-            wait_vmcnt<2 * kPair>();   // the next step's upper and left halves have landed for this wave,
+            wait_vmcnt<kWait>();   // the next step's upper and left halves have landed for this wave,
             lds_barrier();             // and for all; all have read this step's lower and right ones
             quarter(c1, c1, r, c1, c0, oth, [&](int i) {
                 if (i < kCA) copy_a(1, i, cur);
@@ -422,12 +424,11 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
             quarter(c1, c0, l, c0, r, oth + kBl, [&](int i) {
                 if (i < kCB) copy_b(1, i, cur);
             });
-            source(kt + 3);
-            wait_vmcnt<2 * kPair>();   // likewise, the other halves
+            source(kt + STAGES + 1);
+            wait_vmcnt<kWait>();   // likewise, the other halves
             lds_barrier();
-            const uint32_t s = cur;
             cur = oth;
-            oth = s;
+            oth = oth + kStage == lds0 + STAGES * kStage ? lds0 : oth + kStage;
         };
         int kt = s0;
         for (; kt + 1 < s1; kt += 2) {
@@ -508,14 +509,17 @@ __global__ __launch_bounds__(256) void proj_zero_kernel(const ProjArgs p) {
 }
 
 // ---- plan ---------------------------------------------------------------------------------------
-// Tiles: 256 x 256 reach 1.35 PFLOP/s in the main loop, 256 x 128 1.25, 128 x 128 (two workgroups
-// a CU) 1.15; fp32 a tenth of that for any.
+// Tiles, by the rate of the main loop: 256 x 256 reach 1.35 PFLOP/s, 256 x 128 1.25, 128 x 128 1.15
+// with two workgroups a CU; fp32 a tenth of that for any.  The last is for few workgroups with few
+// steps, whose time is the copies' way from memory: four stages, one workgroup a CU.
 struct Tile {
     int bm, bn, slots;     // workgroups of the chip at a time
     double rate;           // PFLOP/s of the main loop
     double tail;           // microseconds of a workgroup that do not overlap with others: first copies, last stores
+    double least;          // microseconds of a step at least: a copy's way through the stages
 };
-constexpr Tile kTiles[3] = {{256, 256, 256, 1.35, 9.0}, {256, 128, 256, 1.25, 6.0}, {128, 128, 512, 1.15, 5.0}};
+constexpr Tile kTiles[4] = {{256, 256, 256, 1.35, 9.0, 1.2}, {256, 128, 256, 1.25, 6.0, 0.7}, {128, 128, 512, 1.15, 5.0, 1.1},
+                            {128, 128, 256, 1.15, 5.0, 0.5}};
 constexpr double kRateF32 = 0.135;
 
 // Sets tiles and how they are cut; returns the tile's number.  All tiles are cut into splits1 parts
@@ -526,16 +530,16 @@ int plan(ProjArgs& a, ProjKind kind, bool bf16) {
     a.steps = (a.red + step - 1) / step * a.phases;
     int best = 0;
     double best_t = 1e30;
-    for (int c = 0; c < 3; ++c) {
+    for (int c = 0; c < 4; ++c) {
         const Tile& t = kTiles[c];
         const int cols = kind == kProjGated ? t.bn / 2 : t.bn;
         long long tiles = 0;
         for (int i = 0; i < a.ngroups; ++i)
             tiles += static_cast<long long>((a.g[i].M + t.bm - 1) / t.bm) * ((a.g[i].N + cols - 1) / cols);
-        // microseconds of so many steps with so many workgroups (two share a CU where there are more than CUs)
+        // microseconds of so many steps with so many workgroups, of which a CU may hold two
         auto time = [&](long long groups, int steps) {
             const double full = 2.0 * t.bm * t.bn * step * 256 / ((bf16 ? t.rate : kRateF32) * 1e9);
-            return steps * full * std::max(1.0, std::min<double>(groups, t.slots) / 256) + t.tail;
+            return steps * std::max(t.least, full * static_cast<double>((std::min<long long>(groups, t.slots) + 255) / 256)) + t.tail;
         };
         for (int s1 = 1; s1 <= 32 && s1 <= std::max(a.steps, 1); ++s1) {
             const long long items = tiles * s1;
@@ -585,19 +589,19 @@ size_t parts_of(const ProjArgs& a) {
     return (a.splits1 > 1 ? t1 * a.splits1 : 0) + (a.splits2 > 1 ? t2 * a.splits2 : 0);
 }
 
-template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int KIND>
+template <typename T, bool AR, bool BR, int BM, int BN, int WM, int WN, int STAGES, int KIND>
 hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
-    constexpr int lds = 2 * (BM + BN) * 128;
+    constexpr int lds = STAGES * (BM + BN) * 128;
     static_assert(lds >= WM * WN * Rows<T, BM, BN, WM, WN, KIND>::kTurn, "turning places");
     const int items = a.tiles1 * a.splits1 + (a.tiles - a.tiles1) * a.splits2;
     static std::once_flag attr_once;   // thread-safe one-time init of the LDS limit
     std::call_once(attr_once, [] {
-        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&proj_kernel<T, AR, BR, BM, BN, WM, WN, KIND>),
+        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&proj_kernel<T, AR, BR, BM, BN, WM, WN, STAGES, KIND>),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     });
     {
         ProfScope prof(kProfProj, st);
-        hipLaunchKernelGGL((proj_kernel<T, AR, BR, BM, BN, WM, WN, KIND>), dim3(items), dim3(64 * WM * WN), lds, st, a);
+        hipLaunchKernelGGL((proj_kernel<T, AR, BR, BM, BN, WM, WN, STAGES, KIND>), dim3(items), dim3(64 * WM * WN), lds, st, a);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || parts_of(a) == 0) return e;
@@ -609,9 +613,10 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
 
 template <typename T, bool AR, bool BR, int KIND>
 hipError_t launch_sized(const ProjArgs& a, int tile, hipStream_t st) {
-    if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, KIND>(a, st);
-    if (tile == 1) return launch_tile<T, AR, BR, 256, 128, 4, 2, KIND>(a, st);
-    return launch_tile<T, AR, BR, 128, 128, 2, 2, KIND>(a, st);
+    if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st);
+    if (tile == 1) return launch_tile<T, AR, BR, 256, 128, 4, 2, 3, KIND>(a, st);
+    if (tile == 2) return launch_tile<T, AR, BR, 128, 128, 2, 2, 2, KIND>(a, st);
+    return launch_tile<T, AR, BR, 128, 128, 2, 2, 4, KIND>(a, st);
 }
 
 template <typename T>

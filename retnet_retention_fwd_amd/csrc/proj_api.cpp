@@ -113,7 +113,7 @@ struct LinearPlan {
 LinearPlan linear_plan(int M, int N, int K, bool bf16, bool aligned) {
     const size_t es = bf16 ? 2 : 4;
     LinearPlan p{};
-    if (retn::proj_small(M)) return p;
+    if (retn::proj_small(M, N)) return p;
     Layout l;
     p.x = l.take(aligned ? 0 : sz(M) * padded(K, bf16) * es);
     p.w = l.take(aligned ? 0 : sz(N) * padded(K, bf16) * es);
@@ -145,7 +145,7 @@ FfnPlan ffn_plan(int M, int D, int F, bool bf16, bool aligned) {
     const size_t es = bf16 ? 2 : 4;
     FfnPlan p{};
     Layout l;
-    if (retn::proj_small(M)) {
+    if (retn::proj_small(M, std::max(D, F))) {
         p.h = l.take(sz(M) * padded(F, bf16) * es);
         p.total = l.total;
         return p;
@@ -313,7 +313,7 @@ retn_status linear_fwd(const void* x, long long ldx, const void* weight, const v
     if (clash(in, outs)) return RETN_ERR_ALIAS;
     if (bad_workspace(workspace, workspace_bytes, p.total)) return RETN_ERR_WORKSPACE;
     Call c{bf16, es, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)};
-    const bool small = retn::proj_small(M);
+    const bool small = retn::proj_small(M, N);
     const Rows rx = small ? Rows{x, ldx} : c.rows(x, ldx, sz(M), K, p.x);
     const Rows rw = small ? Rows{weight, K} : c.rows(weight, K, sz(N), K, p.w);
     const int red = small ? K : padded(K, bf16);
@@ -428,7 +428,7 @@ retn_status gated_ffn_fwd(const void* x, long long ldx, const void* w_gate, cons
     if (clash(in, outs)) return RETN_ERR_ALIAS;
     if (bad_workspace(workspace, workspace_bytes, p.total)) return RETN_ERR_WORKSPACE;
     Call c{bf16, es, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)};
-    const bool small = retn::proj_small(M);
+    const bool small = retn::proj_small(M, std::max(D, F));
     const Rows rx = small ? Rows{x, ldx} : c.rows(x, ldx, sz(M), D, p.x);
     const Rows rg = small ? Rows{w_gate, D} : c.rows(w_gate, D, sz(F), D, p.wg);
     const Rows ru = small ? Rows{w_up, D} : c.rows(w_up, D, sz(F), D, p.wu);

@@ -135,8 +135,9 @@ hipError_t launch_blocks(const ProjArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Rows that one or two blocks hold.
-bool proj_small(int M) { return M <= 32; }
+// One block of rows always (4096 x 4096: 12 us, a cut tile 18); two where the rows, which every
+// workgroup reads, are not more than the weights: 32 rows of 4096 x 4096 15 and 18 us, of 16384 x 2048 26 and 18.
+bool proj_small(int M, int N) { return M <= 16 || (M <= 32 && N <= 4096); }
 
 hipError_t launch_proj_small(const ProjArgs& a, ProjKind kind, bool bf16, hipStream_t st) {
     if (a.g[0].M > 32 || a.g[0].N == 0) return hipErrorInvalidValue;
