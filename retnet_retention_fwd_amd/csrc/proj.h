@@ -63,9 +63,19 @@ hipError_t launch_proj(ProjArgs a, ProjKind kind, bool bf16, bool a_red, bool b_
 bool proj_small(int M, int N);
 hipError_t launch_proj_small(const ProjArgs& a, ProjKind kind, bool bf16, hipStream_t st);
 
-// dst[rows][ldd] = src[rows][lds] of `width` elements, zeros behind them.
-hipError_t launch_proj_pack(const void* src, long long lds, void* dst, long long ldd, size_t rows, int width, bool bf16,
-                            hipStream_t st);
+// Each dst[rows][ldd] = src[rows][lds] of `width` elements, zeros behind them.
+struct PackArgs {
+    struct One {
+        const void* src;
+        long long lds;
+        void* dst;
+        long long ldd;
+        size_t rows;
+        int width;
+    } one[5];
+    int n;
+};
+hipError_t launch_proj_pack(const PackArgs& a, bool bf16, hipStream_t st);
 
 // gz = gy * slope(pre) (act none: not written) and the column sums of it.
 struct SlopeArgs {

@@ -203,17 +203,23 @@ struct Rows {
             for (int j = 0; j < TJ; ++j)
                 *reinterpret_cast<f32x4_t*>(turn + l16 * 64 + ((8 * y + 4 * j + g4) ^ l16) * 4) = acc[y][j];
     }
+    // The lane's rows of block i of half x.
+    __device__ __forceinline__ void rows(int m0, int x, int i, int (&m)[kPass]) const {
+#pragma unroll
+        for (int q = 0; q < kPass; ++q) m[q] = m0 + x * (BM / 2) + (wm * TI + i) * 16 + q * kRows + lane / kUnits;
+    }
     // What follows for the written block i of half x.
-    __device__ __forceinline__ void put(const ProjEpi& e, const ProjGroup& g, int m0, int x, int i) const {
+    __device__ __forceinline__ void put(const ProjEpi& e, const ProjGroup& g, int m0, int x, int i,
+                                        const Reads<T, KIND, kPass>& reads) const {
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         float v[kPass][8], w[kPass][8];
         int m[kPass];
+        rows(m0, x, i, m);
 #pragma unroll
         for (int q = 0; q < kPass; ++q) {
             const int row = q * kRows + lane / kUnits, u = lane % kUnits * 2;
-            m[q] = m0 + x * (BM / 2) + (wm * TI + i) * 16 + row;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const f32x4_t a = *reinterpret_cast<const f32x4_t*>(turn + row * 64 + ((u + k) ^ row) * 4);
@@ -229,7 +235,7 @@ struct Rows {
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        if (n < g.N) finish<T, KIND, kPass>(e, g, cols, m, n, v, w);
+        if (n < g.N) finish<T, KIND, kPass>(e, g, cols, reads, m, n, v, w);
     }
 };
 
@@ -445,13 +451,23 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
         out.init(p.e, g, at.n0, wave, lane, smem);
         // (a loop, as what follows the sums is long: eight copies of it are more than the
         // instruction cache holds, 25 us of 120 at 8192 x 4096 x 1024 with gelu)
+        // What the next block reads is on its way while a block is stored.
+        Reads<T, KIND, Out::kPass> next;
+        int m[Out::kPass];
+        out.rows(at.m0, 0, 0, m);
+        next.load(p.e, g, m, out.n);
 #pragma unroll 1
         for (int b = 0; b < 2 * TI; ++b) {
             const int now = held(b);
+            const Reads<T, KIND, Out::kPass> reads = next;
+            if (now + 1 < 2 * TI) {
+                out.rows(at.m0, (now + 1) / TI, (now + 1) % TI, m);
+                next.load(p.e, g, m, out.n);
+            }
 #pragma unroll
             for (int k = 0; k < 2 * TI; ++k)
                 if (now == k) out.write(acc[k / TI][k % TI]);
-            out.put(p.e, g, at.m0, now / TI, now % TI);
+            out.put(p.e, g, at.m0, now / TI, now % TI, reads);
         }
     } else {
         // a part of a tile's sums, as the lanes hold them
@@ -480,6 +496,12 @@ __global__ __launch_bounds__(64 * WM * WN) void proj_join_kernel(const ProjArgs 
     if (splits == 1) return;
     const Place at = place_of<BM, Out::kCols>(p, t);
     const ProjGroup& g = p.g[at.gi];
+    Out out;
+    out.init(p.e, g, at.n0, wave, lane, smem);
+    Reads<T, KIND, Out::kPass> reads;
+    int m[Out::kPass];
+    out.rows(at.m0, xi / TI, xi % TI, m);
+    reads.load(p.e, g, m, out.n);
     f32x4_t acc[2][TJ];
 #pragma unroll
     for (int y = 0; y < 2; ++y)
@@ -493,10 +515,8 @@ __global__ __launch_bounds__(64 * WM * WN) void proj_join_kernel(const ProjArgs 
 #pragma unroll
             for (int k = 0; k < TJ; ++k) acc[y][k] += o[((xi * 2 + y) * TJ + k) * 64];
     }
-    Out out;
-    out.init(p.e, g, at.n0, wave, lane, smem);
     out.write(acc);
-    out.put(p.e, g, at.m0, xi / TI, xi % TI);
+    out.put(p.e, g, at.m0, xi / TI, xi % TI, reads);
 }
 
 // Products over nothing (no rows in a gradient of weights): zeros.
@@ -637,14 +657,15 @@ hipError_t launch_typed(const ProjArgs& a, int tile, ProjKind kind, bool a_red, 
 
 // ---- packing and slopes ------------------------------------------------------------------------------
 template <typename T>
-__global__ __launch_bounds__(256) void pack_kernel(const T* src, long long lds, T* dst, long long ldd, size_t rows, int width) {
+__global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
     constexpr int V = kPack<T>;
-    const int units = static_cast<int>(ldd / V);
-    const size_t total = rows * units;
+    const PackArgs::One& o = a.one[blockIdx.y];
+    const int units = static_cast<int>(o.ldd / V);
+    const size_t total = o.rows * units;
     for (size_t e = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; e < total; e += static_cast<size_t>(gridDim.x) * 256) {
         const size_t r = e / units;
         const int n = static_cast<int>(e % units) * V;
-        raw_store<T, V>(dst + r * ldd + n, raw_load_n<T, V>(src + r * lds + n, width - n));
+        raw_store<T, V>(static_cast<T*>(o.dst) + r * o.ldd + n, raw_load_n<T, V>(static_cast<const T*>(o.src) + r * o.lds + n, o.width - n));
     }
 }
 
@@ -725,18 +746,16 @@ hipError_t launch_proj(ProjArgs a, ProjKind kind, bool bf16, bool a_red, bool b_
     return bf16 ? launch_typed<bf16_t>(a, tile, kind, a_red, b_red, st) : launch_typed<float>(a, tile, kind, a_red, b_red, st);
 }
 
-hipError_t launch_proj_pack(const void* src, long long lds, void* dst, long long ldd, size_t rows, int width, bool bf16,
-                            hipStream_t st) {
-    const size_t n = rows * static_cast<size_t>(ldd / (bf16 ? 8 : 4));
-    if (n == 0) return hipSuccess;
-    const unsigned blocks = static_cast<unsigned>(std::min<size_t>((n + 255) / 256, 1u << 14));
+hipError_t launch_proj_pack(const PackArgs& a, bool bf16, hipStream_t st) {
+    size_t most = 0;
+    for (int i = 0; i < a.n; ++i) most = std::max(most, a.one[i].rows * static_cast<size_t>(a.one[i].ldd / (bf16 ? 8 : 4)));
+    if (most == 0) return hipSuccess;
+    const dim3 grid(static_cast<unsigned>(std::min<size_t>((most + 255) / 256, 1u << 14)), a.n);
     ProfScope prof(kProfProjPass, st);
     if (bf16)
-        hipLaunchKernelGGL((pack_kernel<bf16_t>), dim3(blocks), dim3(256), 0, st, static_cast<const bf16_t*>(src), lds,
-                           static_cast<bf16_t*>(dst), ldd, rows, width);
+        hipLaunchKernelGGL((pack_kernel<bf16_t>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((pack_kernel<float>), dim3(blocks), dim3(256), 0, st, static_cast<const float*>(src), lds,
-                           static_cast<float*>(dst), ldd, rows, width);
+        hipLaunchKernelGGL((pack_kernel<float>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 

@@ -61,18 +61,25 @@ struct Call {
     hipStream_t st;
     hipError_t err = hipSuccess;
 
-    // The rows as they lie, or laid out at `at` of the workspace with padded widths.
+    retn::PackArgs packs{};
+
+    // The rows as they lie, or where the next `lay` puts them, with padded widths.
     Rows rows(const void* p, long long ld, size_t n, int width, size_t at) {
         if (aligned16(p) && whole(ld, bf16) && whole(width, bf16)) return Rows{p, ld};
         const int w = padded(width, bf16);
-        if (err == hipSuccess) err = retn::launch_proj_pack(p, ld, ws + at, w, n, width, bf16, st);
+        packs.one[packs.n++] = retn::PackArgs::One{p, ld, ws + at, w, n, width};
         return Rows{ws + at, w};
+    }
+    void lay() {
+        if (err == hipSuccess && packs.n > 0) err = retn::launch_proj_pack(packs, bf16, st);
+        packs.n = 0;
     }
     // x W^T of few rows, read as they lie
     void small(const ProjArgs& a, retn::ProjKind kind) {
         if (err == hipSuccess) err = retn::launch_proj_small(a, kind, bf16, st);
     }
     void product(const ProjArgs& a, retn::ProjKind kind, bool a_red, bool b_red) {
+        lay();
         if (err == hipSuccess) err = retn::launch_proj(a, kind, bf16, a_red, b_red, st);
     }
 };
@@ -384,15 +391,18 @@ retn_status linear_bwd(const void* x, long long ldx, const void* weight, const v
         c.err = retn::launch_slope(s, c.st);
     }
     float* const part = reinterpret_cast<float*>(c.ws + p.part);
+    Rows rw{nullptr, 8}, rx{nullptr, 8};
+    if (grad_x != nullptr && M > 0) rw = c.rows(weight, K, sz(N), K, p.w);
+    if (grad_weight != nullptr && M > 0) rx = c.rows(x, ldx, sz(M), K, p.x);
     if (grad_x != nullptr && M > 0) {
         ProjArgs a = product_of(padded(N, bf16), N);
-        a.g[0] = group(gz, c.rows(weight, K, sz(N), K, p.w), grad_x, K, M, K, K);
+        a.g[0] = group(gz, rw, grad_x, K, M, K, K);
         a.part = part;
         c.product(a, retn::kProjLinear, true, false);
     }
     if (grad_weight != nullptr) {
         ProjArgs a = product_of(M, M);
-        a.g[0] = group(gz, M > 0 ? c.rows(x, ldx, sz(M), K, p.x) : Rows{nullptr, 8}, grad_weight, K, N, K, K);
+        a.g[0] = group(gz, rx, grad_weight, K, N, K, K);
         a.part = part;
         c.product(a, retn::kProjLinear, false, false);
     }
@@ -432,6 +442,7 @@ retn_status gated_ffn_fwd(const void* x, long long ldx, const void* w_gate, cons
     const Rows rx = small ? Rows{x, ldx} : c.rows(x, ldx, sz(M), D, p.x);
     const Rows rg = small ? Rows{w_gate, D} : c.rows(w_gate, D, sz(F), D, p.wg);
     const Rows ru = small ? Rows{w_up, D} : c.rows(w_up, D, sz(F), D, p.wu);
+    const Rows rd_w = small ? Rows{w_down, F} : c.rows(w_down, F, sz(D), F, p.wd);
     const int rd = small ? D : padded(D, bf16), rf = padded(F, bf16);
     const Rows h{c.ws + p.h, rf};
     float* const part = reinterpret_cast<float*>(c.ws + p.part);
@@ -450,7 +461,7 @@ retn_status gated_ffn_fwd(const void* x, long long ldx, const void* w_gate, cons
         c.product(a, retn::kProjGated, true, true);
     const int rr = small ? F : rf;
     ProjArgs b = product_of(rr, rr);
-    b.g[0] = group(h, small ? Rows{w_down, F} : c.rows(w_down, F, sz(D), F, p.wd), y, D, M, D, D);
+    b.g[0] = group(h, rd_w, y, D, M, D, D);
     b.e.res = residual;
     b.part = part;
     if (small)
@@ -495,11 +506,17 @@ retn_status gated_ffn_bwd(const void* x, long long ldx, const void* w_gate, cons
     float* const part = reinterpret_cast<float*>(c.ws + p.part);
     const int pd = padded(D, bf16), pf = padded(F, bf16);
     const Rows gg{c.ws + p.gg, pf}, gu{c.ws + p.gu, pf}, h{c.ws + p.h, pf};
-    Rows gy{grad_y, D};
+    Rows gy{grad_y, D}, rx{nullptr, pd}, rg{w_gate, D}, ru{w_up, D};
     if (M > 0) {
         gy = c.rows(grad_y, D, sz(M), D, p.gy);
+        const Rows rw = c.rows(w_down, F, sz(D), F, p.wd);
+        if (grad_x != nullptr) {
+            rg = c.rows(w_gate, D, sz(F), D, p.wg);
+            ru = c.rows(w_up, D, sz(F), D, p.wu);
+        }
+        if (weights) rx = c.rows(x, ldx, sz(M), D, p.x);
         ProjArgs a = product_of(pd, D);
-        a.g[0] = group(gy, c.rows(w_down, F, sz(D), F, p.wd), nullptr, pf, M, pf, F);
+        a.g[0] = group(gy, rw, nullptr, pf, M, pf, F);
         a.e.act = activation;
         a.e.gate = const_cast<void*>(gate);
         a.e.up = const_cast<void*>(up);
@@ -512,7 +529,6 @@ retn_status gated_ffn_bwd(const void* x, long long ldx, const void* w_gate, cons
         c.product(a, retn::kProjGatedBwd, true, false);
     }
     if (grad_x != nullptr && M > 0) {
-        const Rows rg = c.rows(w_gate, D, sz(F), D, p.wg), ru = c.rows(w_up, D, sz(F), D, p.wu);
         ProjArgs a = product_of(pf, F);
         a.phases = 2;
         a.g[0] = group(gg, rg, grad_x, D, M, D, D);
@@ -522,7 +538,6 @@ retn_status gated_ffn_bwd(const void* x, long long ldx, const void* w_gate, cons
         c.product(a, retn::kProjLinear, true, false);
     }
     if (weights) {
-        const Rows rx = M > 0 ? c.rows(x, ldx, sz(M), D, p.x) : Rows{nullptr, pd};
         ProjArgs a = weight_grads(rx, gy, gg, gu, h, grad_w_gate, grad_w_up, grad_w_down, M, D, F);
         a.part = part;
         c.product(a, retn::kProjLinear, false, false);

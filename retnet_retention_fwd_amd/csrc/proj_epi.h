@@ -68,24 +68,48 @@ struct Columns {
         }
     }
 };
-// R rows m[r] of eight adjacent columns n .. n + 7 (`v`, and `w`: the second projection's sums).
-// What a row reads is loaded for all rows first.
-template <typename T, int KIND, int R>
-__device__ __forceinline__ void finish(const ProjEpi& e, const ProjGroup& g, const Columns<T, KIND>& cols, const int (&m)[R], int n,
-                                       float (&v)[R][8], float (&w)[R][8]) {
-    const int left = g.N - n;
-    float x[R][8], u[R][8];
+// Eight adjacent elements as they lie in memory.
+template <typename T>
+struct Eight {
+    static constexpr int V = kPack<T>;
+    Raw<T, V> r[8 / V];
+    __device__ __forceinline__ void load(const T* p, int left) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (m[r] >= g.M) continue;
-        if constexpr (KIND == kProjLinear) {
-            if (e.res != nullptr) load8<T>(static_cast<const T*>(e.res) + static_cast<size_t>(m[r]) * g.N + n, left, x[r]);
-        } else if constexpr (KIND == kProjGatedBwd) {
-            const size_t ga = static_cast<size_t>(m[r]) * e.gate_ld + n;
-            load8<T>(static_cast<const T*>(e.gate) + ga, e.gate_n - n, x[r]);
-            load8<T>(static_cast<const T*>(e.up) + ga, e.gate_n - n, u[r]);
+        for (int i = 0; i < 8 / V; ++i) r[i] = raw_load_n<T, V>(p + i * V, left - i * V);
+    }
+    __device__ __forceinline__ void open(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = up(r[i / V].v[i % V]);
+    }
+};
+// What R rows m[r] read besides the sums: the residual, or gate and up.
+template <typename T, int KIND, int R>
+struct Reads {
+    static constexpr int N = KIND == kProjGated ? 0 : KIND == kProjGatedBwd ? 2 : 1;
+    Eight<T> x[N > 0 ? R : 1], u[N > 1 ? R : 1];
+    __device__ __forceinline__ void load(const ProjEpi& e, const ProjGroup& g, const int (&m)[R], int n) {
+        if constexpr (N > 0) {
+            if (n >= g.N || (KIND == kProjLinear && e.res == nullptr)) return;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (m[r] >= g.M) continue;
+                if constexpr (KIND == kProjLinear) {
+                    x[r].load(static_cast<const T*>(e.res) + static_cast<size_t>(m[r]) * g.N + n, g.N - n);
+                } else {
+                    const size_t at = static_cast<size_t>(m[r]) * e.gate_ld + n;
+                    x[r].load(static_cast<const T*>(e.gate) + at, e.gate_n - n);
+                    u[r].load(static_cast<const T*>(e.up) + at, e.gate_n - n);
+                }
+            }
         }
     }
+};
+// R rows m[r] of eight adjacent columns n .. n + 7 (`v`, and `w`: the second projection's sums).
+template <typename T, int KIND, int R>
+__device__ __forceinline__ void finish(const ProjEpi& e, const ProjGroup& g, const Columns<T, KIND>& cols,
+                                       const Reads<T, KIND, R>& reads, const int (&m)[R], int n, float (&v)[R][8],
+                                       float (&w)[R][8]) {
+    const int left = g.N - n;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         if (m[r] >= g.M) continue;
@@ -97,8 +121,10 @@ __device__ __forceinline__ void finish(const ProjEpi& e, const ProjGroup& g, con
             if (e.pre != nullptr) store8<T>(static_cast<T*>(e.pre) + static_cast<size_t>(m[r]) * g.N + n, v[r], left);
             act_values(v[r], e.act);
             if (e.res != nullptr) {
+                float x[8];
+                reads.x[r].open(x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[r][i] += x[r][i];
+                for (int i = 0; i < 8; ++i) v[r][i] += x[i];
             }
             store8<T>(c, v[r], left);
         } else if constexpr (KIND == kProjGated) {
@@ -111,15 +137,17 @@ __device__ __forceinline__ void finish(const ProjEpi& e, const ProjGroup& g, con
             for (int i = 0; i < 8; ++i) v[r][i] *= w[r][i];
             store8<T>(c, v[r], left);
         } else {
-            float h[8], a[8];
-            act_slopes(x[r], a, e.act);
+            float x[8], u[8], h[8], a[8];
+            reads.x[r].open(x);
+            reads.u[r].open(u);
+            act_slopes(x, a, e.act);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                h[i] = a[i] * u[r][i];
-                x[r][i] *= v[r][i] * u[r][i];
+                h[i] = a[i] * u[i];
+                x[i] *= v[r][i] * u[i];
                 v[r][i] *= a[i];
             }
-            if (e.ggate != nullptr) store8<T>(static_cast<T*>(e.ggate) + ca, x[r], left);
+            if (e.ggate != nullptr) store8<T>(static_cast<T*>(e.ggate) + ca, x, left);
             if (e.gup != nullptr) store8<T>(static_cast<T*>(e.gup) + ca, v[r], left);
             if (e.prod != nullptr) store8<T>(static_cast<T*>(e.prod) + ca, h, left);
         }

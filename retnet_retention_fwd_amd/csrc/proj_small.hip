@@ -111,7 +111,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void proj_small_kernel(const ProjAr
     Columns<T, KIND> cols;
     cols.load(p.e, n, g.N - n);
     const int m[1] = {r};
-    finish<T, KIND, 1>(p.e, g, cols, m, n, v, u);
+    Reads<T, KIND, 1> reads;
+    reads.load(p.e, g, m, n);
+    finish<T, KIND, 1>(p.e, g, cols, reads, m, n, v, u);
 }
 
 template <typename T, int MT, int KIND>
