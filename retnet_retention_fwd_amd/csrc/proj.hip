@@ -451,18 +451,32 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
         out.init(p.e, g, at.n0, wave, lane, smem);
         // (a loop, as what follows the sums is long: eight copies of it are more than the
         // instruction cache holds, 25 us of 120 at 8192 x 4096 x 1024 with gelu)
-        // What the next block reads is on its way while a block is stored.
-        Reads<T, KIND, Out::kPass> next;
-        int m[Out::kPass];
-        out.rows(at.m0, 0, 0, m);
-        next.load(p.e, g, m, out.n);
+        // All that the blocks read besides the sums is loaded in front of the first store (gate and up in
+        // fp32 are too much to hold, and are loaded block by block).
+        typedef Reads<T, KIND, Out::kPass> In;
+        constexpr bool kAhead = In::N > 0 && In::N * 4 * TI * Out::kPass * static_cast<int>(sizeof(T)) <= 64;   // registers
+        In all[kAhead ? 2 * TI : 1], reads;
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < 2 * TI; ++k) {
+                int m[Out::kPass];
+                out.rows(at.m0, k / TI, k % TI, m);
+                all[k].load(p.e, g, m, out.n);
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * TI; ++k) all[k].wait(p.e);
+        }
 #pragma unroll 1
         for (int b = 0; b < 2 * TI; ++b) {
             const int now = held(b);
-            const Reads<T, KIND, Out::kPass> reads = next;
-            if (now + 1 < 2 * TI) {
-                out.rows(at.m0, (now + 1) / TI, (now + 1) % TI, m);
-                next.load(p.e, g, m, out.n);
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int k = 0; k < 2 * TI; ++k)
+                    if (now == k) reads = all[k];
+            } else {
+                int m[Out::kPass];
+                out.rows(at.m0, now / TI, now % TI, m);
+                reads.load(p.e, g, m, out.n);
             }
 #pragma unroll
             for (int k = 0; k < 2 * TI; ++k)
@@ -529,17 +543,17 @@ __global__ __launch_bounds__(256) void proj_zero_kernel(const ProjArgs p) {
 }
 
 // ---- plan ---------------------------------------------------------------------------------------
-// Tiles, by the rate of the main loop: 256 x 256 reach 1.35 PFLOP/s, 256 x 128 1.25, 128 x 128 1.15
-// with two workgroups a CU; fp32 a tenth of that for any.  The last is for few workgroups with few
-// steps, whose time is the copies' way from memory: four stages, one workgroup a CU.
+// Tiles, by the rate of the main loop: 256 x 256 reach 1.35 PFLOP/s, 256 x 128 1.08, 128 x 128 1.15
+// with two workgroups a CU and 0.8 with one; fp32 a tenth of that for any.  The last is for few
+// workgroups with few steps, whose time is the copies' way from memory: four stages, one workgroup a CU.
 struct Tile {
     int bm, bn, slots;     // workgroups of the chip at a time
     double rate;           // PFLOP/s of the main loop
     double tail;           // microseconds of a workgroup that do not overlap with others: first copies, last stores
     double least;          // microseconds of a step at least: a copy's way through the stages
 };
-constexpr Tile kTiles[4] = {{256, 256, 256, 1.35, 9.0, 1.2}, {256, 128, 256, 1.25, 6.0, 0.7}, {128, 128, 512, 1.15, 5.0, 1.1},
-                            {128, 128, 256, 1.15, 5.0, 0.5}};
+constexpr Tile kTiles[4] = {{256, 256, 256, 1.35, 9.0, 1.2}, {256, 128, 256, 1.08, 6.0, 0.7}, {128, 128, 512, 1.15, 5.0, 0.9},
+                            {128, 128, 256, 0.8, 5.0, 0.5}};
 constexpr double kRateF32 = 0.135;
 
 // Sets tiles and how they are cut; returns the tile's number.  All tiles are cut into splits1 parts
@@ -551,6 +565,8 @@ int plan(ProjArgs& a, ProjKind kind, bool bf16) {
     int best = 0;
     double best_t = 1e30;
     for (int c = 0; c < 4; ++c) {
+        // (fp32, and gate and up of a gradient, take more registers than the largest tile leaves)
+        if (c == 0 && (!bf16 || kind == kProjGatedBwd)) continue;
         const Tile& t = kTiles[c];
         const int cols = kind == kProjGated ? t.bn / 2 : t.bn;
         long long tiles = 0;
@@ -558,8 +574,9 @@ int plan(ProjArgs& a, ProjKind kind, bool bf16) {
             tiles += static_cast<long long>((a.g[i].M + t.bm - 1) / t.bm) * ((a.g[i].N + cols - 1) / cols);
         // microseconds of so many steps with so many workgroups, of which a CU may hold two
         auto time = [&](long long groups, int steps) {
-            const double full = 2.0 * t.bm * t.bn * step * 256 / ((bf16 ? t.rate : kRateF32) * 1e9);
-            return steps * std::max(t.least, full * static_cast<double>((std::min<long long>(groups, t.slots) + 255) / 256)) + t.tail;
+            const long long here = (std::min<long long>(groups, t.slots) + 255) / 256;   // workgroups of a CU
+            const double rate = !bf16 ? kRateF32 : t.slots > 256 && here == 1 ? 0.8 : t.rate;
+            return steps * std::max(t.least, 2.0 * t.bm * t.bn * step * 256 * here / (rate * 1e9)) + t.tail;
         };
         for (int s1 = 1; s1 <= 32 && s1 <= std::max(a.steps, 1); ++s1) {
             const long long items = tiles * s1;
@@ -579,7 +596,7 @@ int plan(ProjArgs& a, ProjKind kind, bool bf16) {
                     us = static_cast<double>(items / t.slots) * time(items, per1) + time(t2 * s2, (a.steps + s2 - 1) / s2);
                 }
                 const double parts = (s1 > 1 ? static_cast<double>(t1) * s1 : 0) + (s2 > 1 ? static_cast<double>(t2) * s2 : 0);
-                if (parts > 0) us += 5.0 + parts * t.bm * t.bn * 8 / 3.5e6;
+                if (parts > 0) us += 4.0 + parts * t.bm * t.bn * 8 / 6e6;   // stored and read again, mostly from the caches
                 if (us < best_t) {
                     best_t = us;
                     best = c;
@@ -633,7 +650,9 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
 
 template <typename T, bool AR, bool BR, int KIND>
 hipError_t launch_sized(const ProjArgs& a, int tile, hipStream_t st) {
-    if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st);
+    if constexpr (sizeof(T) == 2 && KIND != kProjGatedBwd) {
+        if (tile == 0) return launch_tile<T, AR, BR, 256, 256, 2, 4, 2, KIND>(a, st);
+    }
     if (tile == 1) return launch_tile<T, AR, BR, 256, 128, 4, 2, 3, KIND>(a, st);
     if (tile == 2) return launch_tile<T, AR, BR, 128, 128, 2, 2, 2, KIND>(a, st);
     return launch_tile<T, AR, BR, 128, 128, 2, 2, 4, KIND>(a, st);

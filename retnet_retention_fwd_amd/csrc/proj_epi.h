@@ -52,6 +52,12 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int left) {
     }
 }
 
+// Waits for a loaded value here.  (Loads and stores count on one counter in their order, so a wait
+// behind stores, or in a loop with them, is one for the stores as well.)
+template <typename V>
+__device__ __forceinline__ void arrived(V& v) {
+    asm volatile("" : "+v"(v));
+}
 // What a lane's eight columns n .. n + 7 have in every row.
 template <typename T, int KIND>
 struct Columns {
@@ -65,6 +71,8 @@ struct Columns {
                 load8<float>(static_cast<const float*>(e.bias) + n, left, bias);
             else
                 load8<T>(static_cast<const T*>(e.bias) + n, left, bias);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) arrived(bias[i]);
         }
     }
 };
@@ -81,12 +89,30 @@ struct Eight {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = up(r[i / V].v[i % V]);
     }
+    __device__ __forceinline__ void wait() {
+#pragma unroll
+        for (int i = 0; i < 8 / V; ++i) {
+            u32x4_t w = __builtin_bit_cast(u32x4_t, r[i]);
+            arrived(w);
+            r[i] = __builtin_bit_cast(decltype(Raw<T, V>{}), w);
+        }
+    }
 };
 // What R rows m[r] read besides the sums: the residual, or gate and up.
 template <typename T, int KIND, int R>
 struct Reads {
     static constexpr int N = KIND == kProjGated ? 0 : KIND == kProjGatedBwd ? 2 : 1;
     Eight<T> x[N > 0 ? R : 1], u[N > 1 ? R : 1];
+    __device__ __forceinline__ void wait(const ProjEpi& e) {
+        if constexpr (N > 0) {
+            if (KIND == kProjLinear && e.res == nullptr) return;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                x[r].wait();
+                if constexpr (N > 1) u[r].wait();
+            }
+        }
+    }
     __device__ __forceinline__ void load(const ProjEpi& e, const ProjGroup& g, const int (&m)[R], int n) {
         if constexpr (N > 0) {
             if (n >= g.N || (KIND == kProjLinear && e.res == nullptr)) return;
