@@ -8,6 +8,8 @@ tensors' device, on its current stream or on `stream`.
 """
 from __future__ import annotations
 
+import functools
+
 from ._block import _binder, _code, _dense, _f, _given, _heads, _i, _ll, _on, _positions, _ptr, _space, _sz, _torch, _vp, _weights
 from ._lib import RETN_BF16, RETN_F32, _check, _require
 
@@ -71,18 +73,31 @@ def _x(x):
     return rows, K, ld, _code(x)
 
 
-def _aligned(code, *widths_and_pointers):
-    """Whether pointers (tensors) and widths (in elements) are multiples of 16 bytes."""
-    unit = 8 if code == RETN_BF16 else 4
-    for w in widths_and_pointers:
-        if w % unit if isinstance(w, int) else w.data_ptr() % 16:
-            return 0
-    return 1
+def _aligned(code, *widths_and_addresses):
+    """Whether widths (in elements, the first three) and addresses are multiples of 16 bytes."""
+    a, b, c, *addresses = widths_and_addresses
+    if (a | b | c) & (7 if code == RETN_BF16 else 3):
+        return 0
+    bits = 0
+    for p in addresses:
+        bits |= p
+    return 0 if bits & 15 else 1
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(name, *sizes):
+    """A workspace query, asked once for the same sizes."""
+    return _fn(name)(*sizes)
 
 
 def _matrix(w, name, x, shape=None):
     """A contiguous weight of x's type and device."""
     if shape is None:
+        try:       # what holds as a rule
+            if w.dtype is x.dtype and w.get_device() == x.get_device() and w.is_contiguous() and w.dim() == 2 and w.shape[0] > 0:
+                return
+        except AttributeError:
+            pass
         _require(w, name, x.dtype, x.device)
         if w.dim() != 2 or w.shape[0] < 1:
             raise ValueError(f"{name} must be [out, in]")
@@ -130,11 +145,12 @@ def linear_fwd(x, weight, bias=None, residual=None, activation="none", return_pr
     on, s = _on(dev, stream)
     with on:
         _given(out, "out", x.dtype, dev, shape)
-        y = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
-        pre = torch.empty(shape, dtype=x.dtype, device=dev) if return_pre else None
-        need = _fn("linear_workspace_bytes")(rows, N, K, code, _aligned(code, x, weight, ld, K, N))
+        y = x.new_empty(shape) if out is None else out
+        pre = x.new_empty(shape) if return_pre else None
+        px, pw = x.data_ptr(), weight.data_ptr()
+        need = _bytes("linear_workspace_bytes", rows, N, K, code, _aligned(code, ld, K, N, px, pw))
         ws, nbytes = _space(need, workspace, dev)
-        _check(_fn("linear_fwd")(_ptr(x), ld, _ptr(weight), _ptr(bias), _ptr(residual), _ptr(y), _ptr(pre), rows, N, K, act,
+        _check(_fn("linear_fwd")(px, ld, pw, _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre), rows, N, K, act,
                                  code, bcode, _ptr(ws), nbytes, s), "linear_fwd")
     return (y, pre) if return_pre else y
 
@@ -163,12 +179,13 @@ def linear_bwd(x, weight, grad_y, pre=None, activation="none", bias_grad=True, x
         raise TypeError(f"bias_dtype must be float32 or {x.dtype}, got {bdtype}")
     on, s = _on(dev, stream)
     with on:
-        gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if x_grad else None
+        gx = x.new_empty(x.shape) if x_grad else None
         gw = torch.empty_like(weight) if weight_grad else None
+        px, pw = x.data_ptr(), weight.data_ptr()
         gb = torch.empty(N, dtype=bdtype, device=dev) if bias_grad else None
-        need = _fn("linear_bwd_workspace_bytes")(rows, N, K, act, code, _aligned(code, x, weight, grad_y, ld, K, N))
+        need = _bytes("linear_bwd_workspace_bytes", rows, N, K, act, code, _aligned(code, ld, K, N, px, pw, grad_y.data_ptr()))
         ws, nbytes = _space(need, workspace, dev)
-        _check(_fn("linear_bwd")(_ptr(x), ld, _ptr(weight), _ptr(pre) if act else None, _ptr(grad_y), _ptr(gx), _ptr(gw),
+        _check(_fn("linear_bwd")(px, ld, pw, _ptr(pre) if act else None, _ptr(grad_y), _ptr(gx), _ptr(gw),
                                  _ptr(gb), rows, N, K, act, code, RETN_F32 if bdtype is torch.float32 else RETN_BF16,
                                  _ptr(ws), nbytes, s), "linear_bwd")
     return gx, gw, gb
@@ -208,13 +225,15 @@ def gated_ffn_fwd(x, w_gate, w_up, w_down, residual=None, activation="silu", ret
     on, s = _on(dev, stream)
     with on:
         _given(out, "out", x.dtype, dev, x.shape)
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        y = x.new_empty(x.shape) if out is None else out
         gate = up = None
         if return_pre:
-            gate, up = (torch.empty(x.shape[:-1] + (F,), dtype=x.dtype, device=dev) for _ in range(2))
-        need = _fn("gated_ffn_workspace_bytes")(rows, D, F, code, _aligned(code, x, w_gate, w_up, w_down, ld, D, F))
+            gate, up = x.new_empty(x.shape[:-1] + (F,)), x.new_empty(x.shape[:-1] + (F,))
+        px = x.data_ptr()
+        addresses = px, w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr()
+        need = _bytes("gated_ffn_workspace_bytes", rows, D, F, code, _aligned(code, ld, D, F, *addresses))
         ws, nbytes = _space(need, workspace, dev)
-        _check(_fn("gated_ffn_fwd")(_ptr(x), ld, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(residual), _ptr(y), _ptr(gate),
+        _check(_fn("gated_ffn_fwd")(px, ld, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(residual), _ptr(y), _ptr(gate),
                                     _ptr(up), rows, D, F, act, code, _ptr(ws), nbytes, s), "gated_ffn_fwd")
     return (y, gate, up) if return_pre else y
 
@@ -233,12 +252,13 @@ def gated_ffn_bwd(x, w_gate, w_up, w_down, gate, up, grad_y, activation="silu", 
     _dense(grad_y, "grad_y", x.dtype, dev, x.shape)
     on, s = _on(dev, stream)
     with on:
-        gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if x_grad else None
+        gx = x.new_empty(x.shape) if x_grad else None
+        px = x.data_ptr()
         gw = [torch.empty_like(w) if weight_grad else None for w in (w_gate, w_up, w_down)]
-        need = _fn("gated_ffn_bwd_workspace_bytes")(rows, D, F, code,
-                                                    _aligned(code, x, w_gate, w_up, w_down, grad_y, ld, D, F))
+        addresses = px, w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), grad_y.data_ptr()
+        need = _bytes("gated_ffn_bwd_workspace_bytes", rows, D, F, code, _aligned(code, ld, D, F, *addresses))
         ws, nbytes = _space(need, workspace, dev)
-        _check(_fn("gated_ffn_bwd")(_ptr(x), ld, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(gate), _ptr(up), _ptr(grad_y),
+        _check(_fn("gated_ffn_bwd")(px, ld, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(gate), _ptr(up), _ptr(grad_y),
                                     _ptr(gx), *map(_ptr, gw), rows, D, F, act, code, _ptr(ws), nbytes, s), "gated_ffn_bwd")
     return (gx, *gw)
 
@@ -327,7 +347,7 @@ def head_norm_rotary_bwd(q, k, table, grad_q, grad_k, q_weight=None, k_weight=No
             out_k, sok = _heads_out(out_k, k, "out_k")
         gqw = torch.empty(d, dtype=wt, device=dev) if q_weight is not None and weight_grad else None
         gkw = torch.empty(d, dtype=wt, device=dev) if k is not None and k_weight is not None and weight_grad else None
-        need = 0 if gqw is None and gkw is None else _fn("head_norm_rotary_bwd_workspace_bytes")(d)
+        need = 0 if gqw is None and gkw is None else _bytes("head_norm_rotary_bwd_workspace_bytes", d)
         ws, nbytes = _space(need, workspace, dev)
         k_in = (None, None, None) if k is None else (_ptr(k), _ptr(grad_k), _ptr(out_k))
         _check(_fn("head_norm_rotary_bwd")(_ptr(q), k_in[0], _ptr(grad_q), k_in[1], _ptr(out_q), k_in[2],

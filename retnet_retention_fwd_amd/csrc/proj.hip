@@ -521,7 +521,7 @@ __global__ __launch_bounds__(64 * WM * WN) void proj_join_kernel(const ProjArgs 
     for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[y][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < splits; ++j) {
         const f32x4_t* o = reinterpret_cast<const f32x4_t*>(p.part) + (part_of(p, t, j) * NW + wave) * (4 * TI * TJ) * 64 + lane;
 #pragma unroll
@@ -556,13 +556,15 @@ constexpr Tile kTiles[4] = {{256, 256, 256, 1.35, 9.0, 1.2}, {256, 128, 256, 1.0
                             {128, 128, 256, 0.8, 5.0, 0.5}};
 constexpr double kRateF32 = 0.135;
 
-// Sets tiles and how they are cut; returns the tile's number.  All tiles are cut into splits1 parts
-// of the reduction; the whole rounds of workgroups that this makes are taken as they are, the rest
-// of the tiles are cut into splits2 parts, as many as fill the chip once.
-int plan(ProjArgs& a, ProjKind kind, bool bf16) {
+// A tile's number and how tiles are cut: all into splits1 parts of the reduction; the whole rounds of
+// workgroups that this makes (tiles1 tiles) are taken as they are, the rest of the tiles are cut into
+// splits2 parts, as many as fill the chip once.
+struct Cut {
+    int tile, tiles1, splits1, splits2;
+};
+Cut best_cut(const ProjArgs& a, ProjKind kind, bool bf16) {
     const int step = bf16 ? 64 : 32;
-    a.steps = (a.red + step - 1) / step * a.phases;
-    int best = 0;
+    Cut best{2, 0, 1, 1};
     double best_t = 1e30;
     for (int c = 0; c < 4; ++c) {
         // (fp32, and gate and up of a gradient, take more registers than the largest tile leaves)
@@ -599,15 +601,39 @@ int plan(ProjArgs& a, ProjKind kind, bool bf16) {
                 if (parts > 0) us += 4.0 + parts * t.bm * t.bn * 8 / 6e6;   // stored and read again, mostly from the caches
                 if (us < best_t) {
                     best_t = us;
-                    best = c;
-                    a.tiles1 = static_cast<int>(t1);
-                    a.splits1 = s1;
-                    a.splits2 = s2;
+                    best = Cut{c, static_cast<int>(t1), s1, s2};
                 }
             }
         }
     }
-    const Tile& t = kTiles[best];
+    return best;
+}
+
+// Sets tiles and cuts; returns the tile's number.  The choice is a function of the sizes alone and takes
+// several microseconds, so a thread keeps those of the sizes that it used last.
+int plan(ProjArgs& a, ProjKind kind, bool bf16) {
+    a.steps = (a.red + (bf16 ? 64 : 32) - 1) / (bf16 ? 64 : 32) * a.phases;
+    struct Entry {
+        int key[9];
+        Cut cut;
+    };
+    static thread_local Entry kept[64];
+    int key[9] = {1 + kind + 4 * (bf16 ? 1 : 0) + 8 * a.ngroups, a.steps};
+    unsigned at = 0;
+    for (int i = 0; i < a.ngroups; ++i) {
+        key[2 + 2 * i] = a.g[i].M;
+        key[3 + 2 * i] = a.g[i].N;
+    }
+    for (int k : key) at = at * 31u + static_cast<unsigned>(k);
+    Entry& e = kept[(at ^ (at >> 15)) % 64];
+    if (!std::equal(key, key + 9, e.key)) {
+        e.cut = best_cut(a, kind, bf16);
+        std::copy(key, key + 9, e.key);
+    }
+    a.tiles1 = e.cut.tiles1;
+    a.splits1 = e.cut.splits1;
+    a.splits2 = e.cut.splits2;
+    const Tile& t = kTiles[e.cut.tile];
     a.band = 8;
     int tiles = 0;
     for (int i = 0; i < a.ngroups; ++i) {
@@ -618,7 +644,7 @@ int plan(ProjArgs& a, ProjKind kind, bool bf16) {
         g.end = tiles;
     }
     a.tiles = tiles;
-    return best;
+    return e.cut.tile;
 }
 // Parts of sums that cut tiles leave.
 size_t parts_of(const ProjArgs& a) {
