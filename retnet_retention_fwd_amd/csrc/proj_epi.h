@@ -130,6 +130,13 @@ struct Reads {
         }
     }
 };
+// Columns of a padded product past gate's and up's are zero also where an infinite operand met the
+// zeros there: the next product reads them.
+__device__ __forceinline__ void no_padding(float (&v)[8], int left) {
+    if (left >= 8) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? v[i] : 0.f;
+}
 // R rows m[r] of eight adjacent columns n .. n + 7 (`v`, and `w`: the second projection's sums).
 template <typename T, int KIND, int R>
 __device__ __forceinline__ void finish(const ProjEpi& e, const ProjGroup& g, const Columns<T, KIND>& cols,
@@ -154,7 +161,8 @@ __device__ __forceinline__ void finish(const ProjEpi& e, const ProjGroup& g, con
             }
             store8<T>(c, v[r], left);
         } else if constexpr (KIND == kProjGated) {
-            // (columns of a padded product past gate's and up's are zero: both sums are)
+            no_padding(v[r], e.gate_n - n);
+            no_padding(w[r], e.gate_n - n);
             const size_t ga = static_cast<size_t>(m[r]) * e.gate_ld + n;
             if (e.gate != nullptr) store8<T>(static_cast<T*>(e.gate) + ga, v[r], e.gate_n - n);
             if (e.up != nullptr) store8<T>(static_cast<T*>(e.up) + ga, w[r], e.gate_n - n);
@@ -166,6 +174,7 @@ __device__ __forceinline__ void finish(const ProjEpi& e, const ProjGroup& g, con
             float x[8], u[8], h[8], a[8];
             reads.x[r].open(x);
             reads.u[r].open(u);
+            no_padding(v[r], e.gate_n - n);
             act_slopes(x, a, e.act);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {

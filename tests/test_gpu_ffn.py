@@ -146,3 +146,22 @@ def test_many_tiles(M, D, F):
              yd.abs().T @ (2.0 ** -8 * 1.01 * h.abs() + 2.0 ** -24 * 24 * gk.abs() * uk.abs()) + n * yd.abs().T @ h.abs())
     for a, b, m in zip(got, refs, rooms):
         assert ((a.double() - b).abs() <= 2.0 ** -8 * b.abs() + 1.05 * m).all()
+
+
+@pytest.mark.parametrize("F", [100, 101, 104])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_infinities_do_not_meet_padding(dtype, F):
+    """Everything positive: an infinity in a row makes that row infinite, not NaN, whether or not
+    the hidden width is a multiple of 16 bytes."""
+    M, D = 40, 72
+    gen = torch.Generator().manual_seed(5)
+    t = lambda *s: (torch.rand(s, generator=gen) * 0.1 + 0.01).to("cuda", TYPES[dtype])
+    x, gy, wg, wu, wd = t(M, D), t(M, D), t(F, D), t(F, D), t(D, F)
+    clean, gate, up = R().gated_ffn_fwd(x, wg, wu, wd, return_pre=True)
+    grad = R().gated_ffn_bwd(x, wg, wu, wd, gate, up, gy)[0]
+    x2, gy2 = x.clone(), gy.clone()
+    x2[39, 3] = gy2[39, 3] = float("inf")
+    y = R().gated_ffn_fwd(x2, wg, wu, wd)
+    assert torch.isposinf(y[39]).all() and torch.equal(y[:39], clean[:39])
+    g = R().gated_ffn_bwd(x, wg, wu, wd, gate, up, gy2)[0]
+    assert torch.isposinf(g[39]).all() and torch.equal(g[:39], grad[:39])
