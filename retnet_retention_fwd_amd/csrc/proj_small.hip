@@ -1,12 +1,13 @@
-// Products of few rows (the tokens of a decoding batch): C = A W^T with at most 64 rows.
+// Products of few rows (the tokens of a decoding batch): C = A W^T with at most 32 rows.
 //
 // Bound by the weights' bytes and by latency: every weight is used for one block of rows only, so
 // it goes from memory straight into the matrix instructions' registers, past LDS.  A workgroup
 // owns 16 columns, and its waves share the reduction: a wave takes every nw-th piece of 64 bytes
-// of the rows, with the loads of eight pieces in flight, and the waves' sums are added in LDS in
+// of the rows, with the loads of eight pieces (four for two blocks of rows) in flight, and the waves' sums are added in LDS in
 // their order.  Rows and widths of any alignment are read as they lie.
 //
-// Measured: one token through the gated block of 1024 x 4096 (25 MB of weights).
+// Measured: one token through the gated block of 1024 x 4096, 17 MB of weights in 6.1 us and 8 MB in 7.7
+// (64 workgroups of 16 waves); a call of 16 rows of 4096 x 4096 takes 11.1 us (3.0 TB/s).
 
 #include "common.h"
 #include "launch.h"
