@@ -662,8 +662,14 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
     constexpr int lds = STAGES * (BM + BN) * 128;
     static_assert(lds >= WM * WN * Rows<T, BM, BN, WM, WN, KIND>::kTurn, "turning places");
     const int items = a.tiles1 * a.splits1 + (a.tiles - a.tiles1) * a.splits2;
-    static std::once_flag attr_once;   // thread-safe one-time init of the LDS limit
-    std::call_once(attr_once, [] {
+    // the LDS limit belongs to a device's function: set once on each, whichever thread comes first
+    constexpr int kDevices = 64;
+    static std::once_flag attr_once[kDevices];
+    int dev = 0;
+    hipError_t err = hipGetDevice(&dev);
+    if (err != hipSuccess) return err;
+    if (dev < 0 || dev >= kDevices) return hipErrorInvalidDevice;
+    std::call_once(attr_once[dev], [] {
         (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&proj_kernel<T, AR, BR, BM, BN, WM, WN, STAGES, KIND>),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     });
@@ -671,8 +677,8 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
         ProfScope prof(kProfProj, st);
         hipLaunchKernelGGL((proj_kernel<T, AR, BR, BM, BN, WM, WN, STAGES, KIND>), dim3(items), dim3(64 * WM * WN), lds, st, a);
     }
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || parts_of(a) == 0) return e;
+    err = hipGetLastError();
+    if (err != hipSuccess || parts_of(a) == 0) return err;
     ProfScope prof(kProfReduce, st);
     hipLaunchKernelGGL((proj_join_kernel<T, BM, BN, WM, WN, KIND>), dim3(a.splits1 > 1 ? a.tiles : a.tiles - a.tiles1, BM / WM / 16),
                        dim3(64 * WM * WN), 0, st, a);
