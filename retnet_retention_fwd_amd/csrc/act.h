@@ -31,6 +31,13 @@ __device__ __forceinline__ float normal_tail(float a, float& e) {
     e = __builtin_amdgcn_exp2f(a * a * (-0.5f * kLog2e));
     return t * p * e;
 }
+// The logistic function p of x, and p (1 - p).  Both from e^-|x|, which is one at most: 1 - p of a p next to one would
+// lose its bits, and a slope takes them |z| times, or behind the cubic argument 30 times and more.
+__device__ __forceinline__ float logistic(float x, float& pq) {
+    const float e = __builtin_amdgcn_exp2f(fabsf(x) * -kLog2e), big = rcp(1.f + e), small = e * big;
+    pq = big * small;
+    return x > 0.f ? big : small;
+}
 // 2 sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh(./2)) / 2 is its logistic function.
 __device__ __forceinline__ float tanh_arg(float z) {
     return 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);
@@ -64,13 +71,15 @@ __device__ __forceinline__ float act_slope(float z, float& value) {
         value = z * p;
         return fmaf(c * 0.3989422804014327f, e, p);
     } else if constexpr (ACT == RETN_ACT_GELU_TANH) {
-        const float c = cut(z, 16.f), p = sigmoid_f(tanh_arg(c));
+        float pq;
+        const float c = cut(z, 16.f), p = logistic(tanh_arg(c), pq);
         value = z * p;
-        return fmaf(c * p * (1.f - p), 1.5957691216057308f * fmaf(3.f * 0.044715f * c, c, 1.f), p);
+        return fmaf(c * pq, 1.5957691216057308f * fmaf(3.f * 0.044715f * c, c, 1.f), p);
     } else {
-        const float c = cut(z, 100.f), p = sigmoid_f(c);
+        float pq;
+        const float c = cut(z, 100.f), p = logistic(c, pq);
         value = z * p;
-        return fmaf(c * p, 1.f - p, p);
+        return fmaf(c, pq, p);
     }
 }
 template <int ACT>

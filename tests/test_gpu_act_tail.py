@@ -87,7 +87,7 @@ def test_values_of_the_gradient(act, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", SMOOTH)
 def test_slopes(act, dtype):
     print(f"\n[case] slopes {act} {dtype}", flush=True)
     z, zr = grid(dtype)
