@@ -67,8 +67,8 @@ __device__ __forceinline__ float act_slope(float z, float& value) {
     } else if constexpr (ACT == RETN_ACT_GELU) {
         const float c = cut(z, 16.f);
         float e;
-        const float q = normal_tail(fabsf(c), e), p = c > 0.f ? 1.f - q : q;
-        value = z * p;
+        const float a = fabsf(c), q = normal_tail(a, e), p = c > 0.f ? 1.f - q : q;
+        value = fmaf(-a, q, z <= 0.f ? 0.f : z);     // as the forward's, also at the infinities
         return fmaf(c * 0.3989422804014327f, e, p);
     } else if constexpr (ACT == RETN_ACT_GELU_TANH) {
         float pq;

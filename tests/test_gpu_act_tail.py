@@ -98,3 +98,22 @@ def test_slopes(act, dtype):
     terms = np.abs(p) + np.abs(ref - p)
     inside(got, ref, np.where(zr < 0, (steps(zr, act) + 8) * terms, 24) * U + half(TYPES[dtype]) * np.abs(ref)
            + (1 + np.abs(zr) * growth(zr, act)) * T)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["none", "relu"] + SMOOTH)
+def test_both_directions_agree_at_the_ends_of_the_type(act, dtype):
+    """Where P is 0, 1/2 or 1, the gated product that the gradient of w_down forms again is the forward's, NaN where
+    that is NaN: a gate of minus infinity, whose gelu is 0, leaves the gradients finite."""
+    print(f"\n[case] ends {act} {dtype}", flush=True)
+    t = TYPES[dtype]
+    gate = torch.tensor([float("-inf"), -3e38, -1e4, -0.0, 0.0, 1e4, 3e38, float("inf"), float("nan")], device="cuda").to(t)
+    F = len(gate)
+    x, one, row = (torch.ones(s, device="cuda", dtype=t) for s in ((1, 1), (F, 1), (1, F)))
+    forward = R().linear_fwd(gate[:, None], x, activation=act)[:, 0]
+    gx, _, _, gwd = R().gated_ffn_bwd(x, one, one, row, gate[None], row, x, activation=act)
+    both = torch.isnan(forward) & torch.isnan(gwd[0])
+    assert (both | (forward == gwd[0])).all(), (forward, gwd)
+    if act in ("relu", "gelu"):
+        gx = R().gated_ffn_bwd(x, one[:1], one[:1], row[:, :1], gate[None, :1], row[:, :1], x, activation=act)[0]
+        assert gx.item() == 0.0
