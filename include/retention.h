@@ -280,8 +280,9 @@ int retention_abi_version(void);
  * Kinds: 0 matrix-core chunkwise pass, 1 its segment-state pre-pass, 2 its segment
  * scan, 3 generic chunkwise kernel, 4 decode step, 5 state copy (empty sequence), 6 layer
  * normalisation, 7 rotary positions, 8 causal convolution, 9 selective scan, 10 its passes
- * over segments and tiles before that, 11 sums of partial gradients and of split products, 12
- * projections, 13 their passes over single tensors, 14 head norms with rotary positions.
+ * over segments and tiles before that, 11 sums of partial gradients, 12 projections, 13 their
+ * passes over single tensors, 14 head norms with rotary positions, 15 sums of split projections
+ * with what follows them.
  * Errors: RETN_ERR_SHAPE (nkinds < 0), RETN_ERR_NULL, RETN_ERR_HIP.
  */
 retn_status retention_profile_enable(int on);

@@ -75,7 +75,7 @@ EXPORTED = (
 # Kernel kinds reported by retention_profile_read.
 PROFILE_KINDS = ("chunk_main", "chunk_prepass", "chunk_scan", "chunk_generic", "decode", "state_copy", "layer_norm",
                  "rotary", "causal_conv", "selective_scan", "selective_scan_prepass", "gradient_sums",
-                 "projection", "projection_pass", "head_norm_rotary")
+                 "projection", "projection_pass", "head_norm_rotary", "projection_join")
 
 
 class RetentionError(RuntimeError):

@@ -193,7 +193,7 @@ hipError_t run_msr(const MsrShape& s, const MsrPtrs& x, const MsrPlan& p, void* 
 // Optional per-kernel timing (HIP events around each launch, see profile.cpp).
 enum ProfKind { kProfMain = 0, kProfPre = 1, kProfScan = 2, kProfGeneric = 3, kProfDecode = 4, kProfCopy = 5,
                 kProfNorm = 6, kProfRotary = 7, kProfConv = 8, kProfSelScan = 9, kProfScanPre = 10, kProfReduce = 11,
-                kProfProj = 12, kProfProjPass = 13, kProfHeads = 14, kProfKinds = 15 };
+                kProfProj = 12, kProfProjPass = 13, kProfHeads = 14, kProfProjJoin = 15, kProfKinds = 16 };
 bool prof_enabled();
 hipError_t prof_enable(bool on);
 hipError_t prof_read(double* ms, int* count, int nkinds, int* dropped);

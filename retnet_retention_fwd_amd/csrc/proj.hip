@@ -679,7 +679,7 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t st) {
     }
     err = hipGetLastError();
     if (err != hipSuccess || parts_of(a) == 0) return err;
-    ProfScope prof(kProfReduce, st);
+    ProfScope prof(kProfProjJoin, st);
     hipLaunchKernelGGL((proj_join_kernel<T, BM, BN, WM, WN, KIND>), dim3(a.splits1 > 1 ? a.tiles : a.tiles - a.tiles1, BM / WM / 16),
                        dim3(64 * WM * WN), 0, st, a);
     return hipGetLastError();
