@@ -726,7 +726,9 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
 }
 
 // Lanes of a wave lie over units of eight columns, lpr of them a row; a workgroup takes a
-// strip of 8 lpr columns and a chunk of rows, and leaves one row of partial sums.
+// strip of 8 lpr columns and a chunk of rows, and leaves one row of partial sums.  In bf16 gz is rounded to bf16, which
+// is what the products take (gradients behind an activation: 2.3e-3 off instead of 1.7e-3, relative to 64 bits); the
+// column sums are of the values before that.
 struct SlopePlan {
     int lpr, strips, chunks;
     size_t per;

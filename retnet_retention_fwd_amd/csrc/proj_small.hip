@@ -3,11 +3,13 @@
 // Bound by the weights' bytes and by latency: every weight is used for one block of rows only, so
 // it goes from memory straight into the matrix instructions' registers, past LDS.  A workgroup
 // owns 16 columns, and its waves share the reduction: a wave takes every nw-th piece of 64 bytes
-// of the rows, with the loads of eight pieces (four for two blocks of rows) in flight, and the waves' sums are added in LDS in
-// their order.  Rows and widths of any alignment are read as they lie.
+// of the rows, eight pieces (four for two blocks of rows) at a time with all their loads in flight while it has
+// that many left, then one at a time; the waves' sums are added in LDS in their order.  A wave's share is short
+// where the reduction is: of 1024 bf16 elements over eight waves, or 2048 over sixteen, it is four pieces, which one
+// block of rows takes singly.  Rows and widths of any alignment are read as they lie.
 //
 // Measured: one token through the gated block of 1024 x 4096, 17 MB of weights in 6.1 us and 8 MB in 7.7
-// (64 workgroups of 16 waves); a call of 16 rows of 4096 x 4096 takes 11.1 us (3.0 TB/s).
+// (64 workgroups of 16 waves on 256 CUs); 16 rows of 4096 x 4096 in 12.4 us with weights that no cache holds (2.7 TB/s).
 
 #include "common.h"
 #include "launch.h"
@@ -120,7 +122,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void proj_small_kernel(const ProjAr
 template <typename T, int MT, int KIND>
 hipError_t launch_rows(const ProjArgs& a, hipStream_t st) {
     constexpr int kStep = 64 / static_cast<int>(sizeof(T));
-    // waves of a workgroup: each has four pieces at least; more than eight where few workgroups share the chip
+    // waves of a workgroup, with more than two pieces each (all of one wave's where there are four or less);
+    // more than eight waves where few workgroups share the chip
     const int pieces = (a.red_rows + kStep - 1) / kStep, groups = (a.g[0].N + 15) / 16;
     int nw = 1;
     while (nw < (groups <= 256 ? kMaxWaves : 8) && nw * 4 < pieces) nw *= 2;
@@ -138,8 +141,12 @@ hipError_t launch_blocks(const ProjArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// One block of rows always (4096 x 4096: 12 us, a cut tile 18); two where the rows, which every
-// workgroup reads, are not more than the weights: 32 rows of 4096 x 4096 15 and 18 us, of 16384 x 2048 26 and 18.
+// One block of rows always (16 rows of 4096 x 4096: 12 us; a cut tile takes 18 for any number up to 128).  Two blocks
+// up to 4096 columns, as every workgroup reads all rows again: 32 rows of N columns x K, here and with a cut tile,
+// in us, bf16: 1024 x 1024 5 and 11, 4096 x 1024 6 and 14, 4096 x 4096 15 and 19; 16384 x 2048 27 and 23, 16384 x 8192 95 and
+// 79.  The border is by columns alone and coarse: up to it, reductions of 8192 are faster with a tile (2048 x 8192 26 and
+// 20, 4096 x 8192 28 and 24); beyond it short ones would be faster here (8192 x 2048 16 and 19), and fp32 at any size (16384 x
+// 8192 210 and 276).
 bool proj_small(int M, int N) { return M <= 16 || (M <= 32 && N <= 4096); }
 
 hipError_t launch_proj_small(const ProjArgs& a, ProjKind kind, bool bf16, hipStream_t st) {
