@@ -20,7 +20,7 @@
 // transposed in memory.
 //
 // Bound by the matrix cores in the main loop: 8192^3 bf16 runs at 1.32 to 1.41 PFLOP/s in any order of
-// the operands (811, 785 and 791 us; the matrix cores busy 74% of the cycles), the rest goes to the
+// the operands (811, 785 and 791 us; the matrix cores busy 72 to 74% of the cycles), the rest goes to the
 // barriers, where the older wave of a SIMD waits for the younger.  Short reductions are bound by the
 // tails, in which a CU's one workgroup stores (8192 x 4096 x 1024: 70 us, 89 with gelu and two outputs).
 
